@@ -366,6 +366,95 @@ int lrkv_dense_decode_attn(const lrkv_dense_cache *cache, const void *q,
                            void *workspace, size_t workspace_bytes,
                            void *stream);
 
+/* Full-rank paged cache held in 8 bits: next to the dense bf16 cache above,
+ * half its bytes (LowRAM abstract: cache compression composes with
+ * quantisation; the pages give no scheme).  A block is the LRKV_PAGE_TOKENS
+ * tokens of one page, of one KV head and side (keys or values), and has one
+ * fp32 scale.  It is quantised once, when its last token arrives, so what is
+ * stored does not depend on how the tokens were split into calls:
+ *   a = max(max |x|, 2^-100),  M = 127 (LRKV_CODE_INT8) or 448
+ *   (LRKV_CODE_E4M3), s = a / M rounded to fp32, and the code of x is M x / a
+ *   rounded half to even, to a whole number or to e4m3 (4 exponent and 3
+ *   mantissa bits); a code stands for code * s.
+ * A block holding an infinity or a NaN gets codes 0 and s = NaN: all its
+ * values read as NaN.  The tokens of the block that is not full yet stay
+ * bf16 in `tail`.
+ *
+ * pages[num_pages][num_kv_heads] slabs of LRKV_QUANT_SLAB_BYTES:
+ *   8192 bytes of key codes: dim d of token t at 128 t + 16 (c ^ 4 (t & 1))
+ *     + d % 16, c = d / 16 (odd tokens swap the halves of their row);
+ *   8192 bytes of value codes, transposed: dim d of token t at 64 d + t;
+ *   fp32 key scale, fp32 value scale, 24 zero bytes.
+ * An int8 code q is stored as the byte q + 128, an e4m3 code as itself.
+ * Block j of sequence b lives in page block_table[b * max_pages_per_seq + j].
+ *
+ * tail[batch][num_kv_heads][2][LRKV_QUANT_TAIL][128] bf16, keys then values:
+ * token t in slot t % LRKV_QUANT_TAIL.  It holds the open block and the one
+ * before it, so seq_len may be set back by up to LRKV_PAGE_TOKENS tokens
+ * (drafted tokens that were rejected); the next append goes on from there.
+ *
+ * The rules on block_table and append_counter are those of lrkv_cache.  The
+ * kernels set *error once and never clear it: 2 = a block-table entry out of
+ * range (never dereferenced: the write is skipped, the block's tokens are
+ * left out of attention, its rows read as 0), 1 = a bounded wait timed out,
+ * 3 = tokens past the capacity of max_pages_per_seq pages (dropped). */
+enum { LRKV_CODE_INT8 = 0, LRKV_CODE_E4M3 = 1 };
+#define LRKV_QUANT_TAIL 128
+#define LRKV_QUANT_SLAB_BYTES 16416
+typedef struct lrkv_quant_cache {
+  int32_t batch;              /* B, 1..LRKV_MAX_BATCH                     */
+  int32_t num_kv_heads;       /* H_kv                                     */
+  int32_t head_dim;           /* must be 128                              */
+  int32_t code;               /* LRKV_CODE_INT8 or LRKV_CODE_E4M3         */
+  int32_t num_pages;          /* pages in the pool                        */
+  int32_t max_pages_per_seq;  /* row length of block_table                */
+  void *pages;                /* slabs, 16-byte aligned                   */
+  const int32_t *block_table; /* [batch][max_pages_per_seq] page ids      */
+  void *tail;                 /* open blocks, 16-byte aligned             */
+  int32_t *seq_len;           /* [batch] tokens appended so far           */
+  int32_t *append_counter;    /* [batch] zero-initialised scratch         */
+  int32_t *error;             /* one error word, zero it at creation      */
+} lrkv_quant_cache;
+
+/* Append bf16 tokens (n_new as for lrkv_compress) and advance seq_len; the
+ * blocks that become full are quantised.  Token i of (b, h) starts at
+ * k + b*seq_stride + h*head_stride + i*token_stride (element strides,
+ * multiples of 8, the same for v); k and v 16-byte aligned.
+ * LRKV_ERR_CAPACITY when n_tokens alone exceeds the pages' capacity.  One
+ * launch. */
+int lrkv_quant_append(const lrkv_quant_cache *cache, const void *k, const void *v,
+                      int32_t n_tokens, const int32_t *n_new, int64_t seq_stride,
+                      int64_t head_stride, int64_t token_stride, void *stream);
+
+/* Read tokens back: row i of (b, h) becomes the values of token first[b] + i
+ * (first NULL: token i) as dtype LRKV_F32 (code * s in fp32) or LRKV_BF16
+ * (that, rounded once); rows of tokens the sequence does not have are left as
+ * they were.  Strides in elements of dtype, multiples of 16 bytes; k and v
+ * 16-byte aligned.  One launch. */
+int lrkv_quant_read(const lrkv_quant_cache *cache, const int32_t *first, int32_t n_tokens,
+                    void *k, void *v, int32_t dtype, int64_t seq_stride, int64_t head_stride,
+                    int64_t token_stride, void *stream);
+
+/* Attention over the cache as it stands (the new tokens already appended),
+ * causal: sequence b has n = min(n_q[b], n_queries) queries (n_q NULL:
+ * n_queries); its query i stands at position seq_len[b] - n + i and sees the
+ * tokens up to there; a query that sees none gets o = 0.  Rows of o past n
+ * are left as they were.
+ *   q, o : bf16 rows of 128; query i of (b, q head h) at q + b*q_seq_stride +
+ *          h*q_head_stride + i*q_token_stride (elements, multiples of 8;
+ *          likewise o); 16-byte aligned, o apart from q.  q head h reads KV head
+ *          h / (num_q_heads / num_kv_heads), any whole ratio up to 128.
+ *   workspace : at least lrkv_quant_attn_workspace_bytes, 16-byte aligned,
+ *          zeroed when allocated (the calls leave their counters at zero);
+ *          calls sharing a workspace must be stream-ordered. */
+size_t lrkv_quant_attn_workspace_bytes(const lrkv_quant_cache *cache, int32_t num_q_heads,
+                                       int32_t n_queries);
+int lrkv_quant_attn(const lrkv_quant_cache *cache, const void *q, int32_t num_q_heads,
+                    int32_t n_queries, const int32_t *n_q, int64_t q_seq_stride,
+                    int64_t q_head_stride, int64_t q_token_stride, float scale, void *o,
+                    int64_t o_seq_stride, int64_t o_head_stride, int64_t o_token_stride,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static text for a status code. */
 const char *lrkv_status_string(int status);
 

@@ -19,6 +19,8 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblrkv.so
 
 LRKV_BF16, LRKV_F32, LRKV_BF16_Q8, LRKV_BF16_VA = 0, 1, 2, 3
 VA_KEEP = 16
+QUANT_CODES = {"int8": 0, "e4m3": 1}
+QUANT_TAIL, QUANT_SLAB_BYTES = 128, 16416
 HEAD_DIM = 128
 PAGE_TOKENS = 64
 FULL_RANK_TILE = 32
@@ -53,13 +55,24 @@ class DenseDesc(ctypes.Structure):
                 ("append_counter", ctypes.c_void_p)]
 
 
+class QuantDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("code", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+                ("pages", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("tail", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("append_counter", ctypes.c_void_p), ("error", ctypes.c_void_p)]
+
+
 EXPORTS = ["lrkv_compress", "lrkv_decode_workspace_bytes", "lrkv_decode_attn",
            "lrkv_oja_update", "lrkv_qr_orthonormalize", "lrkv_dense_append",
            "lrkv_dense_decode_workspace_bytes", "lrkv_dense_decode_attn",
            "lrkv_status_string", "lrkv_version", "lrkv_decode_attn_static",
            "lrkv_rebase_workspace_bytes", "lrkv_rebase", "lrkv_oja_update_chunked",
            "lrkv_compress_amortised", "lrkv_amortise_workspace_bytes", "lrkv_amortise",
-           "lrkv_decode_attn_amortised", "lrkv_decode_step"]
+           "lrkv_decode_attn_amortised", "lrkv_decode_step",
+           "lrkv_quant_append", "lrkv_quant_read", "lrkv_quant_attn_workspace_bytes",
+           "lrkv_quant_attn"]
 
 
 def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
@@ -90,6 +103,11 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
         "lrkv_amortise": (ctypes.c_int, [P, P, I32, I64, I64, P, I64, P, P, SZ, P]),
         "lrkv_decode_attn_amortised": (ctypes.c_int,
                                        [P, P, I32, P, P, I64, P, F32, P, P, SZ, P]),
+        "lrkv_quant_append": (ctypes.c_int, [P, P, P, I32, P, I64, I64, I64, P]),
+        "lrkv_quant_read": (ctypes.c_int, [P, P, I32, P, P, I32, I64, I64, I64, P]),
+        "lrkv_quant_attn_workspace_bytes": (SZ, [P, I32, I32]),
+        "lrkv_quant_attn": (ctypes.c_int, [P, P, I32, I32, P, I64, I64, I64, F32, P, I64, I64,
+                                           I64, P, SZ, P]),
         "lrkv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "lrkv_version": (ctypes.c_int, []),
     }
@@ -400,6 +418,137 @@ def dense_decode_attn(cache: DenseCache, q: torch.Tensor, scale: float, o: torch
     _check("lrkv_dense_decode_attn", _lib.lrkv_dense_decode_attn(
         ctypes.byref(cache.desc), _ptr(q), q.shape[1], float(scale), _ptr(o), _ptr(workspace),
         workspace.numel(), _stream(stream)))
+    return o
+
+
+class QuantCache:
+    """Device buffers of one full-rank cache held in 8 bits, laid out as
+    include/lrkv.h says: bf16 tokens, quantised block by block (64 tokens of
+    one KV head and side share a scale) to code "int8" or "e4m3".
+
+    max_tokens bounds the tokens per sequence (rounded up to whole pages);
+    the block table maps each sequence's pages into a shared pool (identity
+    order unless a permutation of range(num_pages) is given).
+    """
+
+    def __init__(self, B: int, H_kv: int, max_tokens: int, code: str = "int8", device="cuda",
+                 page_perm: Optional[torch.Tensor] = None):
+        if code not in QUANT_CODES:
+            raise ValueError(f"code must be one of {sorted(QUANT_CODES)}, not {code!r}")
+        self.B, self.H_kv, self.code, self.dtype = B, H_kv, code, torch.bfloat16
+        self.max_pages = max(1, math.ceil(max_tokens / PAGE_TOKENS))
+        self.num_pages = B * self.max_pages
+        self.pages = torch.zeros((self.num_pages, H_kv, QUANT_SLAB_BYTES), dtype=torch.uint8,
+                                 device=device)
+        self.device = self.pages.device
+        ids = torch.arange(self.num_pages, dtype=torch.int32) if page_perm is None else \
+            torch.as_tensor(page_perm, dtype=torch.int32)
+        self.block_table = ids.reshape(B, self.max_pages).to(device)
+        self.tail = torch.zeros((B, H_kv, 2, QUANT_TAIL, HEAD_DIM), dtype=torch.bfloat16,
+                                device=device)
+        self.seq_len = torch.zeros(B, dtype=torch.int32, device=device)
+        self.append_counter = torch.zeros(B, dtype=torch.int32, device=device)
+        self.error_word = torch.zeros(1, dtype=torch.int32, device=device)
+        self.desc = QuantDesc(B, H_kv, HEAD_DIM, QUANT_CODES[code], self.num_pages,
+                              self.max_pages, self.pages.data_ptr(), self.block_table.data_ptr(),
+                              self.tail.data_ptr(), self.seq_len.data_ptr(),
+                              self.append_counter.data_ptr(), self.error_word.data_ptr())
+
+    def error(self) -> int:
+        """Error word of the calls so far (0 = ok; waits for them)."""
+        return int(self.error_word.item())
+
+
+def _quant_rows(name: str, cache: QuantCache, x: torch.Tensor, heads: int, dtype):
+    """Strides (sequence, head, token) of rows [B, heads, n, 128]."""
+    if x.dim() != 4 or x.shape[0] != cache.B or x.shape[1] != heads or x.shape[3] != HEAD_DIM:
+        raise ValueError(f"{name} must be [{cache.B}, {heads}, n, {HEAD_DIM}], "
+                         f"not {list(x.shape)}")
+    if x.dtype != dtype or x.device != cache.device:
+        raise ValueError(f"{name} must be {dtype} on {cache.device}, not {x.dtype} on {x.device}")
+    if x.stride(3) != 1 or x.shape[2] > 0 and min(x.stride()[:3]) < 0:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    # a dimension of one entry has no stride of its own
+    return tuple(x.stride(i) if x.shape[i] > 1 else 0 for i in range(3))
+
+
+def _quant_counts(name: str, cache: QuantCache, t: Optional[torch.Tensor]):
+    if t is not None and (t.dtype != torch.int32 or t.device != cache.device or
+                          t.shape != (cache.B,) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous int32 [{cache.B}] on {cache.device}")
+    return _ptr(t)
+
+
+def quant_append(cache: QuantCache, k: torch.Tensor, v: torch.Tensor,
+                 n_new: Optional[torch.Tensor] = None, stream=None) -> None:
+    """lrkv_quant_append: append bf16 k, v [B, H_kv, n, 128] (any strides with
+    contiguous rows, the same for both; n_new[b] <= n tokens of sequence b
+    when given)."""
+    st = _quant_rows("k", cache, k, cache.H_kv, torch.bfloat16)
+    if _quant_rows("v", cache, v, cache.H_kv, torch.bfloat16) != st or k.shape != v.shape:
+        raise ValueError("k and v must have the same shape and strides")
+    counts = _quant_counts("n_new", cache, n_new)
+    with torch.cuda.device(cache.device):
+        _check("lrkv_quant_append", _lib.lrkv_quant_append(
+            ctypes.byref(cache.desc), _ptr(k), _ptr(v), k.shape[2], counts, *st,
+            _stream(stream)))
+
+
+def quant_read(cache: QuantCache, k: torch.Tensor, v: torch.Tensor,
+               first: Optional[torch.Tensor] = None, stream=None):
+    """lrkv_quant_read: write the values of tokens first[b] .. first[b] + n - 1
+    (from token 0 when first is None) into k, v [B, H_kv, n, 128], fp32 or
+    bf16; rows of tokens that do not exist are left as they were."""
+    if k.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"k must be bf16 or fp32, not {k.dtype}")
+    st = _quant_rows("k", cache, k, cache.H_kv, k.dtype)
+    if _quant_rows("v", cache, v, cache.H_kv, k.dtype) != st or k.shape != v.shape:
+        raise ValueError("k and v must have the same shape and strides")
+    if any(n > 1 and s == 0 for n, s in zip(k.shape, st)):
+        raise ValueError("k and v are written: their rows may not overlap")
+    counts = _quant_counts("first", cache, first)
+    with torch.cuda.device(cache.device):
+        _check("lrkv_quant_read", _lib.lrkv_quant_read(
+            ctypes.byref(cache.desc), counts, k.shape[2], _ptr(k), _ptr(v),
+            _dtype_code(k.dtype), *st, _stream(stream)))
+    return k, v
+
+
+def quant_attn_workspace(cache: QuantCache, num_q_heads: int, n_queries: int = 1) -> torch.Tensor:
+    """Zero-filled workspace for quant_attn calls of up to n_queries queries
+    per sequence (the library keeps its counters at zero)."""
+    with torch.cuda.device(cache.device):
+        n = int(_lib.lrkv_quant_attn_workspace_bytes(ctypes.byref(cache.desc), num_q_heads,
+                                                     n_queries))
+    if n == 0:
+        raise LrkvError("lrkv_quant_attn_workspace_bytes", -2)
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+
+
+def quant_attn(cache: QuantCache, q: torch.Tensor, scale: float, o: torch.Tensor,
+               workspace: torch.Tensor, n_q: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """lrkv_quant_attn: causal attention of the last n (n_q[b] <= n when
+    given) tokens' queries q [B, H_q, n, 128], or [B, H_q, 128] for one, into
+    o of the same shape; bf16, any strides with contiguous rows."""
+    if o.shape != q.shape:
+        raise ValueError("q and o must have the same shape")
+    q4, o4 = (q.unsqueeze(2), o.unsqueeze(2)) if q.dim() == 3 else (q, o)
+    heads = q4.shape[1] if q4.dim() == 4 else 0
+    qst = _quant_rows("q", cache, q4, heads, torch.bfloat16)
+    ost = _quant_rows("o", cache, o4, heads, torch.bfloat16)
+    if any(n > 1 and s == 0 for n, s in zip(o4.shape, ost)):
+        raise ValueError("o is written: its rows may not overlap")
+    if o.data_ptr() == q.data_ptr() and o.numel():
+        raise ValueError("o may not be q: q is read while o is written")
+    if workspace.device != cache.device or not workspace.is_contiguous() or \
+            workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace must be contiguous uint8 on {cache.device}")
+    counts = _quant_counts("n_q", cache, n_q)
+    with torch.cuda.device(cache.device):
+        _check("lrkv_quant_attn", _lib.lrkv_quant_attn(
+            ctypes.byref(cache.desc), _ptr(q4), heads, q4.shape[2], counts, *qst, float(scale),
+            _ptr(o4), *ost, _ptr(workspace), workspace.numel(), _stream(stream)))
     return o
 
 
