@@ -85,17 +85,20 @@ class QuantCacheOracle:
     def attend(self, q, scale: float, n_q=None):
         """o [B, H_q, n, 128] (NaN rows past a sequence's queries) and, for the
         tests' error bounds, w = sum p |v| of the same shape and
-        s [B, H_q, n, 2]: the largest sum |q k| * scale and |score| of a row."""
+        s [B, H_q, n, 3]: a row's largest sum |q k| * scale, its largest
+        |score| and its largest p * (largest |v| of the token's block)."""
         q = np.asarray(q, np.float64)
         B, Hq, n, _ = q.shape
         G = Hq // self.H
         o, w = np.full(q.shape, np.nan), np.zeros(q.shape)
-        s2 = np.zeros((B, Hq, n, 2))
+        s2 = np.zeros((B, Hq, n, 3))
         for b in range(B):
             L = self.length(b)
             m = n if n_q is None else int(np.clip(n_q[b], 0, n))
             for h in range(self.H):
                 K, V = self.values(b, h, 0), self.values(b, h, 1)
+                top = np.concatenate([np.full(min(BLOCK, L - j), np.max(np.abs(V[j:j + BLOCK])))
+                                      for j in range(0, L, BLOCK)] or [np.zeros(0)])
                 for g in range(h * G, h * G + G):
                     for i in range(m):
                         seen = L - m + i + 1
@@ -108,5 +111,5 @@ class QuantCacheOracle:
                         o[b, g, i] = p @ V[:seen]
                         w[b, g, i] = p @ np.abs(V[:seen])
                         s2[b, g, i] = (np.max(np.abs(K[:seen]) @ np.abs(q[b, g, i])) * scale,
-                                       np.max(np.abs(s)))
+                                       np.max(np.abs(s)), np.max(p * top[:seen]))
         return o, w, s2

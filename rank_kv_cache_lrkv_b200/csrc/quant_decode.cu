@@ -1,0 +1,694 @@
+// Attention of few query rows over the 8-bit full-rank cache.
+//
+// Row r of a unit (sequence, KV head) is query r / G of q head h G + r % G.
+// A code is an exact fp16 number, so with q brought to fp16 (exactly: times
+// a power of two that puts its row's largest element in [2^14, 2^15); what
+// is 2^-28 of that and less loses bits) and the block's scales kept outside,
+//   score = (q . c_k) (s_k scale 2^e),  acc += (p s_v) c_v
+// run on mma.sync m16n8k16 with fp32 accumulation.  Besides the softmax's
+// running maximum m a row keeps M', the running maximum of a block's largest
+// score + floor(log2 s_v): the weights 2^(score - M') s_v 2^13 are then at
+// most 2^14 whatever the blocks' scales, are rounded to fp16 once and keep
+// eleven bits down to 2^-27 of the largest.
+//
+// One launch, persistent, one CTA per SM.  The blocks of all (unit, row
+// group)s are laid end to end and each CTA takes an equal contiguous range.
+//  * W consumer warps take every W-th block.  Each keeps D page slabs (codes
+//    and scales, one bulk copy each) of its own in flight and refills a stage
+//    as soon as it has read it, so no warp waits for another's page.
+//    S^T = C_k q^T: A fragments are the code bytes themselves, a lane reading 16 bytes of a token's row
+//    (which dims form a 16-wide step is free, as long as q agrees) and
+//    widening them in registers; V is stored transposed, so acc^T = C_v^T P^T
+//    reads its A fragments the same way; P^T moves into the B operand by
+//    movmatrix.  Tokens are dealt to A rows so that this lands them in the
+//    order of the V bytes: row i of step s is token 16 (i / 2) + 4 s + i % 2
+//    (+ 2 for rows 8..15);
+//  * tail warp: the open block's bf16 rows, straight from global memory, on
+//    bf16 MMAs with the weights split in two bf16 halves.
+// At the end of a unit's part the warps' (m, l, acc) are combined in
+// shared memory.  A unit in one CTA is finished there; otherwise the parts
+// go to the workspace and the unit's last CTA to arrive folds them in order
+// (so the result does not depend on which was last) and zeroes the counter.
+#include "quant.cuh"
+#include "tcgen05.cuh"
+
+namespace lrkv {
+
+namespace {
+
+constexpr int kPad = kHeadDim + 4;              // combine rows: no bank conflicts
+constexpr float kBoost = 8192.f;                // 2^13
+
+struct DecPlan {
+  int slots, ml, full, start, len, nq, misc, total;
+};
+__host__ __device__ inline DecPlan dec_plan(int W, int D, int rows, int B) {
+  DecPlan p;
+  p.slots = W * D * kQSlab;
+  p.ml = p.slots + (W + 1) * rows * kPad * 4;
+  p.full = p.ml + (W + 1) * rows * 16;
+  p.start = p.full + W * D * 8;
+  p.len = p.start + (B + 1) * 8;
+  p.nq = p.len + B * 4;
+  p.misc = p.nq + B * 4;
+  p.total = p.misc + 16;
+  return p;
+}
+
+// Workspace: a counter per CTA, then two records of [16][132] fp32 (m, l, M',
+// -, 128 sums) per CTA.  Of the units that a CTA shares with others one at
+// most begins in it and one at most began before it: they have record 1 and
+// record 0, and the unit's counter is that of the CTA in which it begins.
+// Nothing depends on the call's sizes, so any call may follow any other.
+constexpr int kMaxRows = 16;
+__host__ __device__ inline size_t dec_records(int C) { return ((size_t)C * 4 + 255) / 256 * 256; }
+__host__ __device__ inline size_t dec_ws(int C) {
+  return dec_records(C) + (size_t)C * 2 * kMaxRows * kPad * 4;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_b16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Over the 8 lanes that share lane % 4.
+__device__ __forceinline__ float col_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+__device__ __forceinline__ float col_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
+
+// A part of a unit: its place, the blocks [i0, i1) of `tiles` in this CTA's
+// range, and the line's index of its block 0.
+struct Part {
+  int b, h, rg, tiles, i0, i1;
+  long long first;
+};
+
+template <bool kE4M3, int NT, int W, int D>
+__global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttnArgs a) {
+  constexpr int kRows = 8 * NT;
+  extern __shared__ __align__(128) uint8_t sm[];
+  const QuantView& c = a.c;
+  const DecPlan pl = dec_plan(W, D, kRows, c.B);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + pl.full);
+  float* slots = reinterpret_cast<float*>(sm + pl.slots);
+  float4* ml = reinterpret_cast<float4*>(sm + pl.ml);  // [W + 1][kRows] (m, l, M')
+  long long* start = reinterpret_cast<long long*>(sm + pl.start);
+  int* slen = reinterpret_cast<int*>(sm + pl.len);
+  int* snq = reinterpret_cast<int*>(sm + pl.nq);
+  volatile int* fail = reinterpret_cast<volatile int*>(sm + pl.misc);
+  volatile int* lastflag = fail + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  if (threadIdx.x == 0) {
+    *fail = 0;
+    for (int s = 0; s < W * D; ++s) mbar_init(&full[s], 1);
+    mbar_fence_init();
+  }
+  pdl_trigger();
+  pdl_wait();
+  if (warp == W) {
+    // blocks before each sequence; a sequence without tokens still has one
+    // (empty) block for its queries' zeros
+    const int per = (c.B + 31) / 32, b0 = min(c.B, lane * per), b1 = min(c.B, b0 + per);
+    long long own = 0;
+    for (int b = b0; b < b1; ++b) {
+      slen[b] = quant_len(c, b);
+      snq[b] = quant_queries(a, b);
+      const int groups = (snq[b] * a.G + kRows - 1) / kRows;
+      own += (long long)max(1, (slen[b] + kQBlock - 1) / kQBlock) * groups * c.H;
+    }
+    long long incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    long long e = incl - own;
+    for (int b = b0; b < b1; ++b) {
+      start[b] = e;
+      const int groups = (snq[b] * a.G + kRows - 1) / kRows;
+      e += (long long)max(1, (slen[b] + kQBlock - 1) / kQBlock) * groups * c.H;
+    }
+    if (lane == 31) start[c.B] = incl;
+  }
+  __syncthreads();
+  const long long total = start[c.B];
+  // no CTA without a block: the parts of a unit are counted as CTAs
+  const int C = (int)min((long long)gridDim.x, total);
+  if ((int)blockIdx.x >= C) return;
+  const long long lo = total * blockIdx.x / C, hi = total * (blockIdx.x + 1) / C;
+
+  // the part that block x of the line belongs to, cut to [lo, hi)
+  auto part_of = [&](long long x) {
+    Part p;
+    int l = 0, r = c.B;
+    while (r - l > 1) {
+      const int mid = (l + r) >> 1;
+      if (start[mid] <= x) l = mid; else r = mid;
+    }
+    p.b = l;
+    p.tiles = max(1, (slen[l] + kQBlock - 1) / kQBlock);
+    const int groups = (snq[l] * a.G + kRows - 1) / kRows;
+    const long long in = x - start[l];
+    const int u = (int)(in / p.tiles);
+    p.h = u / groups;
+    p.rg = u - p.h * groups;
+    p.first = start[l] + (long long)u * p.tiles;
+    p.i0 = (int)(max(lo, p.first) - p.first);
+    p.i1 = (int)(min(hi, p.first + p.tiles) - p.first);
+    return p;
+  };
+
+  // ---------------- consumer: the loads it has in flight
+  uint8_t* ring = sm + warp * D * kQSlab;
+  uint64_t* bar = full + warp * D;
+  int n_issued = 0, n_read = 0;      // slabs asked for, slabs used
+  uint32_t bad = 0;                  // stages whose page was out of range
+  long long xi = lo + warp;          // next block to ask for
+  Part pi;                           // its part (the last one looked up)
+  if (warp < W && xi < hi) pi = part_of(xi);
+  // next full block at or after xi; its page id is loaded here and first
+  // looked at by the issue() after this one
+  int npage = -1, nhead = 0;
+  auto find_next = [&]() {
+    while (xi < hi) {
+      if (xi >= pi.first + pi.i1) pi = part_of(xi);
+      const int i = (int)(xi - pi.first);
+      if ((i + 1) * kQBlock <= slen[pi.b]) {
+        npage = __ldg(c.bt + (size_t)pi.b * c.maxp + i);
+        nhead = pi.h;
+        return true;
+      }
+      xi += W;
+    }
+    return false;
+  };
+  const uint64_t pol = l2_evict_first_policy();
+  bool more = false;
+  auto issue = [&]() {
+    if (!more) return;
+    const int s = n_issued % D;
+    if (npage >= 0 && npage < c.num_pages) {
+      bad &= ~(1u << s);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar[s], kQSlab);
+        bulk_g2s_hint(ring + s * kQSlab, c.pages + ((size_t)npage * c.H + nhead) * kQSlab, kQSlab,
+                      &bar[s], pol);
+      }
+    } else {
+      bad |= 1u << s;
+      if (lane == 0) {
+        quant_error(c, kErrBadPage);
+        mbar_arrive(&bar[s]);
+      }
+    }
+    ++n_issued;
+    xi += W;
+    more = find_next();
+  };
+  if (warp < W) {
+    more = find_next();
+#pragma unroll
+    for (int s = 0; s < D; ++s) issue();
+  }
+
+  int* counters = static_cast<int*>(a.ws);
+  float* records = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + dec_records(gridDim.x));
+
+  for (long long x = lo; x < hi;) {
+    const Part p = part_of(x);
+    const int L = slen[p.b], nq = snq[p.b], R = nq * a.G;
+    const int r0 = p.rg * kRows, rows = min(kRows, R - r0);
+    const int pos0 = L - nq;  // position of query 0
+    const int minpos = pos0 + r0 / a.G;
+    const __nv_bfloat16* qb = a.q + p.b * a.qs + (long long)(p.h * a.G) * a.qh;
+    auto qrow = [&](int r) { return qb + (long long)(r % a.G) * a.qh + (long long)(r / a.G) * a.qt; };
+    float m[2 * NT], l[2 * NT], mv[2 * NT], acc[8][NT][4];
+    int pos[2 * NT];
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+      m[i] = mv[i] = -INFINITY;
+      l[i] = 0.f;
+      // this lane's columns: row 8 (i / 2) + 2 t + i % 2
+      const int r = 8 * (i >> 1) + 2 * t + (i & 1);
+      pos[i] = r < rows ? pos0 + (r0 + r) / a.G : 0x7fffffff;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][n][e] = 0.f;
+    float acc_scale = 1.f;  // acc's unit in the end
+    bool any = false;
+
+    if (warp < W) {
+      // ---------------- quantised blocks
+      long long xc = x + ((warp - (int)((x - lo) % W)) + W) % W;
+      const long long xend = p.first + p.i1;
+      const bool have = xc < xend && ((int)(xc - p.first) + 1) * kQBlock <= L;
+      if (have) {
+        any = true;
+        // q's B fragments, fp16, and the columns' factors
+        uint32_t qf[NT][8][2];
+        float fcol[2 * NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint4 w[4];
+          const int r = 8 * n + g;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
+          if (r < rows) {
+            const uint4* src = reinterpret_cast<const uint4*>(qrow(r0 + r));
+            w[0] = __ldg(src + 2 * t);
+            w[1] = __ldg(src + 2 * t + 1);
+            w[2] = __ldg(src + 8 + 2 * t);
+            w[3] = __ldg(src + 9 + 2 * t);
+          }
+          uint32_t mx = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mx = __vmaxu2(mx, w[i].x & 0x7fff7fffu);
+            mx = __vmaxu2(mx, w[i].y & 0x7fff7fffu);
+            mx = __vmaxu2(mx, w[i].z & 0x7fff7fffu);
+            mx = __vmaxu2(mx, w[i].w & 0x7fff7fffu);
+          }
+          mx = max(mx >> 16, mx & 0xffffu);
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          // exponent of the row's largest element; not finite: as it is
+          int e = (int)(mx >> 7) - 127;
+          e = mx == 0 || e == 128 ? 14 : max(e, -100);
+          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+          const float down = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              qf[n][2 * i + (k >> 1)][k & 1] = pack_f16x2(bf_lo(v[k]) * up, bf_hi(v[k]) * up);
+          }
+          fcol[2 * n] = __shfl_sync(0xffffffffu, down, 8 * t) * (a.scale * kLog2e);
+          fcol[2 * n + 1] = __shfl_sync(0xffffffffu, down, 8 * t + 4) * (a.scale * kLog2e);
+        }
+        for (; xc < xend; xc += W) {
+          const int i = (int)(xc - p.first);
+          if ((i + 1) * kQBlock > L) break;
+          const int s = n_read % D;
+          const bool ok = tc_wait_warp(&bar[s], (n_read / D) & 1, fail, lane);
+          const bool use = ok && !((bad >> s) & 1);
+          ++n_read;
+          if (use) {
+            const uint8_t* slab = ring + s * kQSlab;
+            const float2 sc = *reinterpret_cast<const float2*>(slab + 2 * kQSide);
+            // ---- scores: sacc[s4][n]: tokens 16 (g / 2) + 4 s4 + g % 2 (+ 2)
+            float sacc[4][NT][4];
+#pragma unroll
+            for (int s4 = 0; s4 < 4; ++s4) {
+              const int ta = 16 * (g >> 1) + 4 * s4 + (g & 1);
+              const uint8_t* ra = slab + ta * kHeadDim + ((t ^ ((g & 1) << 2)) << 4);
+              const uint8_t* rb = slab + ta * kHeadDim + ((t ^ 4 ^ ((g & 1) << 2)) << 4);
+              uint4 ka[2], kb[2];
+              ka[0] = *reinterpret_cast<const uint4*>(ra);
+              kb[0] = *reinterpret_cast<const uint4*>(ra + 2 * kHeadDim);
+              ka[1] = *reinterpret_cast<const uint4*>(rb);
+              kb[1] = *reinterpret_cast<const uint4*>(rb + 2 * kHeadDim);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sacc[s4][n][e] = 0.f;
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t wa[4] = {ka[hf].x, ka[hf].y, ka[hf].z, ka[hf].w};
+                const uint32_t wb[4] = {kb[hf].x, kb[hf].y, kb[hf].z, kb[hf].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  uint32_t a0, a1, a2, a3;
+                  quant_half4<kE4M3>(wa[k], a0, a2);
+                  quant_half4<kE4M3>(wb[k], a1, a3);
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+                    mma_f16(sacc[s4][n], a0, a1, a2, a3, qf[n][4 * hf + k][0], qf[n][4 * hf + k][1]);
+                }
+              }
+            }
+            // ---- softmax: one maximum per column and block
+            const int base = i * kQBlock;
+            const bool edge = base + kQBlock - 1 > minpos;
+            float corr[2 * NT];
+            bool moved = false;
+            // s_v = 2^ev fv, 1 <= fv < 2 (a NaN stays in fv)
+            const uint32_t vbits = __float_as_uint(sc.y);
+            const bool vnan = sc.y != sc.y;
+            const float ev = vnan ? 0.f : (float)((int)(vbits >> 23) - 127);
+            const float fv = vnan ? sc.y : __uint_as_float((vbits & 0x7fffffu) | 0x3f800000u);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float f = fcol[2 * n + j] * sc.x;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int s4 = 0; s4 < 4; ++s4)
+#pragma unroll
+                  for (int u = 0; u < 2; ++u) {
+                    float& v = sacc[s4][n][2 * u + j];
+                    v *= f;
+                    if (edge && base + 16 * (g >> 1) + 4 * s4 + (g & 1) + 2 * u > pos[2 * n + j])
+                      v = -INFINITY;
+                    mx = fmaxf(mx, v);
+                  }
+                mx = col_max(mx);
+                const float mvn = fmaxf(mv[2 * n + j], mx + ev);
+                mx = fmaxf(mx, m[2 * n + j]);
+                const float ref = mx == -INFINITY ? 0.f : mx;
+                const float vref = mvn == -INFINITY ? 0.f : mvn;
+                const float cr = ex2_approx(m[2 * n + j] - ref);
+                moved |= mvn != mv[2 * n + j];
+                corr[2 * n + j] = ex2_approx(mv[2 * n + j] - vref);
+                m[2 * n + j] = mx;
+                mv[2 * n + j] = mvn;
+                // 2^(m - M') s_v 2^13 (no more than 2^126: p is 0 there)
+                const float wmul = fv * ex2_approx(fminf(ref + ev - vref, 112.f) + 13.f);
+                float sum = 0.f;
+#pragma unroll
+                for (int s4 = 0; s4 < 4; ++s4)
+#pragma unroll
+                  for (int u = 0; u < 2; ++u) {
+                    float& v = sacc[s4][n][2 * u + j];
+                    const bool out = edge && v == -INFINITY;
+                    v = ex2_approx(v - ref);
+                    sum += v;
+                    v = out ? 0.f : v * wmul;  // a NaN scale does not reach what is masked
+                  }
+                l[2 * n + j] = l[2 * n + j] * cr + sum;
+              }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) acc[j][n][e] *= corr[2 * n + (e & 1)];
+            }
+            uint32_t pb[4][NT][2];
+#pragma unroll
+            for (int s4 = 0; s4 < 4; ++s4)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                  pb[s4][n][u] =
+                      movmatrix_trans(pack_f16x2(sacc[s4][n][2 * u], sacc[s4][n][2 * u + 1]));
+            // ---- values: dims 16 j + g (+ 8), tokens 16 t .. 16 t + 15
+            const uint8_t* vs = slab + kQSide + g * kQBlock + t * 16;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint4 va = *reinterpret_cast<const uint4*>(vs + 16 * j * kQBlock);
+              const uint4 vb = *reinterpret_cast<const uint4*>(vs + (16 * j + 8) * kQBlock);
+              const uint32_t wa[4] = {va.x, va.y, va.z, va.w};
+              const uint32_t wb[4] = {vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+              for (int s4 = 0; s4 < 4; ++s4) {
+                uint32_t a0, a1, a2, a3;
+                quant_half4<kE4M3>(wa[s4], a0, a2);
+                quant_half4<kE4M3>(wb[s4], a1, a3);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  mma_f16(acc[j][n], a0, a1, a2, a3, pb[s4][n][0], pb[s4][n][1]);
+              }
+            }
+          }
+          __syncwarp();  // the stage is read: refill it
+          if (ok) issue();
+        }
+        acc_scale = 1.f / kBoost;
+      }
+    } else if (p.i1 == p.tiles && L % kQBlock != 0) {
+      // ---------------- the open block, tokens base .. L - 1
+      any = true;
+      const int base = L / kQBlock * kQBlock;
+      const __nv_bfloat16* kt = quant_tail(c, p.b, p.h, 0, base);
+      const __nv_bfloat16* vt = quant_tail(c, p.b, p.h, 1, base);
+      float sacc[4][NT][4];
+#pragma unroll
+      for (int s4 = 0; s4 < 4; ++s4)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sacc[s4][n][e] = 0.f;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int u4 = 0; u4 < 4; ++u4) {  // dims 32 u4 + 8 t .. + 7 of this lane
+        uint4 qw[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          qw[n] = 8 * n + g < rows
+                      ? __ldg(reinterpret_cast<const uint4*>(qrow(r0 + 8 * n + g)) + 4 * u4 + t)
+                      : zero;
+#pragma unroll
+        for (int s4 = 0; s4 < 4; ++s4) {
+          const int ta = 16 * (g >> 1) + 4 * s4 + (g & 1), tb = ta + 2;
+          const uint4 ka = base + ta < L
+                               ? *(reinterpret_cast<const uint4*>(kt + ta * kHeadDim) + 4 * u4 + t)
+                               : zero;
+          const uint4 kb = base + tb < L
+                               ? *(reinterpret_cast<const uint4*>(kt + tb * kHeadDim) + 4 * u4 + t)
+                               : zero;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_b16(sacc[s4][n], ka.x, kb.x, ka.y, kb.y, qw[n].x, qw[n].y);
+            mma_b16(sacc[s4][n], ka.z, kb.z, ka.w, kb.w, qw[n].z, qw[n].w);
+          }
+        }
+      }
+      const float f = a.scale * kLog2e;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float mx = -INFINITY;
+          const int last = min(pos[2 * n + j], L - 1);
+#pragma unroll
+          for (int s4 = 0; s4 < 4; ++s4)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float& v = sacc[s4][n][2 * u + j];
+              v = base + 16 * (g >> 1) + 4 * s4 + (g & 1) + 2 * u > last ? -INFINITY : v * f;
+              mx = fmaxf(mx, v);
+            }
+          mx = col_max(mx);
+          m[2 * n + j] = mv[2 * n + j] = mx;
+          const float ref = mx == -INFINITY ? 0.f : mx;
+          float sum = 0.f;
+#pragma unroll
+          for (int s4 = 0; s4 < 4; ++s4)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float& v = sacc[s4][n][2 * u + j];
+              v = ex2_approx(v - ref);
+              sum += v;
+            }
+          l[2 * n + j] = sum;
+        }
+#pragma unroll
+      for (int s4 = 0; s4 < 4; ++s4) {
+        uint32_t ph[NT][2], pw[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float x0 = sacc[s4][n][2 * u], x1 = sacc[s4][n][2 * u + 1];
+            const uint32_t hi2 = pack_bf16x2(x0, x1);
+            ph[n][u] = movmatrix_trans(hi2);
+            pw[n][u] = movmatrix_trans(pack_bf16x2(x0 - bf_lo(hi2), x1 - bf_hi(hi2)));
+          }
+        // dims 8 g + i (half 0) and 64 + 8 g + i (half 1) of tokens 16 t + 4 s4 ..
+#pragma unroll
+        for (int q2 = 0; q2 < 2; ++q2) {  // 4 dims at a time
+          uint2 v[4][2];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int tok = 16 * t + 4 * s4 + k;
+              v[k][hf] = base + tok < L
+                             ? *reinterpret_cast<const uint2*>(vt + tok * kHeadDim + 64 * hf + 8 * g +
+                                                               4 * q2)
+                             : make_uint2(0, 0);
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t sel = (i & 1) ? 0x7632 : 0x5410;
+            auto pick = [&](int k, int hf) { return (i >> 1) ? v[k][hf].y : v[k][hf].x; };
+            const uint32_t a0 = __byte_perm(pick(0, 0), pick(1, 0), sel);
+            const uint32_t a1 = __byte_perm(pick(0, 1), pick(1, 1), sel);
+            const uint32_t a2 = __byte_perm(pick(2, 0), pick(3, 0), sel);
+            const uint32_t a3 = __byte_perm(pick(2, 1), pick(3, 1), sel);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_b16(acc[4 * q2 + i][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
+              mma_b16(acc[4 * q2 + i][n], a0, a1, a2, a3, pw[n][0], pw[n][1]);
+            }
+          }
+        }
+      }
+    }
+
+    // ---------------- combine the warps' (m, l, M', acc)
+    __syncthreads();  // the slots of the part before are read
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = 8 * n + 2 * t + j;
+        const float ls = col_sum(l[2 * n + j]);
+        if (g == 0) ml[warp * kRows + r] = make_float4(m[2 * n + j], ls, mv[2 * n + j], 0.f);
+        if (any) {
+          float* dst = slots + ((size_t)warp * kRows + r) * kPad;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int d0 = warp < W ? 16 * q + g : 8 * g + q;
+            dst[d0] = acc[q][n][j] * acc_scale;
+            dst[d0 + (warp < W ? 8 : 64)] = acc[q][n][2 + j] * acc_scale;
+          }
+        }
+      }
+    __syncthreads();
+    const bool whole = p.i0 == 0 && p.i1 == p.tiles;
+    // record of this unit's part in CTA cc (c0: the CTA that it begins in)
+    auto record = [&](int cc, bool begins) {
+      return reinterpret_cast<float4*>(records + ((size_t)2 * cc + (begins ? 1 : 0)) * kMaxRows * kPad);
+    };
+    // a row's result, or zeros where it saw nothing: lane's 4 dims
+    auto finish = [&](int r, const float4& st, const float4& o) {
+      const int rr = r0 + r;
+      __nv_bfloat16* dst = a.o + p.b * a.os + (long long)(p.h * a.G + rr % a.G) * a.oh +
+                           (long long)(rr / a.G) * a.ot + 4 * lane;
+      const float f = st.y == 0.f ? 0.f : ex2_approx(st.z - st.x) / st.y;
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+    };
+    // fold one part's (st, s) into (S, o); a part that saw nothing (a NaN sum
+    // is something) adds nothing
+    auto fold = [&](float4& S, float4& o, const float4& st, const float4& s) {
+      if (st.x == -INFINITY && st.y == 0.f) return;
+      const float mn = fmaxf(S.x, st.x), ref = mn == -INFINITY ? 0.f : mn;
+      const float zn = fmaxf(S.z, st.z), zref = zn == -INFINITY ? 0.f : zn;
+      S.y = S.y * ex2_approx(S.x - ref) + st.y * ex2_approx(st.x - ref);
+      const float f0 = ex2_approx(S.z - zref), f1 = ex2_approx(st.z - zref);
+      S.x = mn;
+      S.z = zn;
+      o.x = o.x * f0 + s.x * f1;
+      o.y = o.y * f0 + s.y * f1;
+      o.z = o.z * f0 + s.z * f1;
+      o.w = o.w * f0 + s.w * f1;
+    };
+    const float4 none = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    for (int r = warp; r < rows; r += W + 1) {
+      float4 S = none, o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w <= W; ++w)
+        fold(S, o, ml[w * kRows + r],
+             *reinterpret_cast<const float4*>(slots + ((size_t)w * kRows + r) * kPad + 4 * lane));
+      if (whole) {
+        finish(r, S, o);
+      } else {
+        float4* dst = record(blockIdx.x, p.i0 == 0) + r * (kPad / 4);
+        if (lane == 0) dst[0] = S;
+        dst[1 + lane] = o;
+      }
+    }
+    if (!whole) {
+      // CTAs that hold blocks of this unit: block y lies in CTA
+      // ((y + 1) C - 1) / total
+      const int c0 = (int)(((p.first + 1) * C - 1) / total);
+      const int c1 = (int)(((p.first + p.tiles) * C - 1) / total);
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const int before = atomicAdd(&counters[c0], 1);
+        *lastflag = before == c1 - c0;
+        if (before == c1 - c0) counters[c0] = 0;
+      }
+      __syncthreads();
+      if (*lastflag) {
+        __threadfence();
+        for (int r = warp; r < rows; r += W + 1) {
+          float4 S = none, o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int cc = c0; cc <= c1; ++cc) {
+            const float4* src = record(cc, cc == c0) + r * (kPad / 4);
+            fold(S, o, __ldcg(src), __ldcg(src + 1 + lane));
+          }
+          finish(r, S, o);
+        }
+      }
+    }
+    x = p.first + p.i1;
+  }
+  if (*fail) {
+    // copies still landing end before the CTA does
+    if (warp < W && lane == 0) {
+      const uint64_t t0 = global_ns();
+      for (int k = n_read; k < n_issued; ++k)
+        while (!mbar_try_wait(&bar[k % D], (k / D) & 1) && global_ns() - t0 < kTcTimeoutNs) {
+        }
+      quant_error(c, kErrTimeout);
+    }
+  }
+}
+
+}  // namespace
+
+// Rows per group, and the kernel for them.
+template <bool kE4M3, int NT, int W, int D>
+static int launch(const QuantAttnArgs& a, const DevInfo& info, cudaStream_t st) {
+  const void* fn = (const void*)quant_decode_kernel<kE4M3, NT, W, D>;
+  const int smem = dec_plan(W, D, 8 * NT, a.c.B).total;
+  if (smem > info.optin) return LRKV_ERR_UNSUPPORTED;
+  const int rc = prepare_kernel(fn, true);
+  if (rc != LRKV_OK) return rc;
+  QuantAttnArgs args = a;
+  void* p[] = {&args};
+  return launch_pdl(fn, dim3(info.sms), dim3((W + 1) * 32), smem, st, p) == cudaSuccess
+             ? LRKV_OK
+             : LRKV_ERR_CUDA;
+}
+
+size_t quant_attn_workspace(int, int, int, int) {
+  int dev = 0;
+  DevInfo info;
+  return current_device_info(dev, info) == LRKV_OK ? dec_ws(info.sms) : 0;
+}
+
+int quant_attn_launch(const QuantAttnArgs& a, cudaStream_t st) {
+  int dev = 0;
+  DevInfo info;
+  const int rc = current_device_info(dev, info);
+  if (rc != LRKV_OK) return rc;
+  if ((long long)a.n * a.G <= 8)
+    return a.c.e4m3 ? launch<true, 1, 5, 2>(a, info, st) : launch<false, 1, 5, 2>(a, info, st);
+  return a.c.e4m3 ? launch<true, 2, 4, 2>(a, info, st) : launch<false, 2, 4, 2>(a, info, st);
+}
+
+}  // namespace lrkv

@@ -453,30 +453,63 @@ class QuantCache:
                               self.max_pages, self.pages.data_ptr(), self.block_table.data_ptr(),
                               self.tail.data_ptr(), self.seq_len.data_ptr(),
                               self.append_counter.data_ptr(), self.error_word.data_ptr())
+        self.desc_ref = ctypes.byref(self.desc)
 
     def error(self) -> int:
         """Error word of the calls so far (0 = ok; waits for them)."""
         return int(self.error_word.item())
 
 
+# These checks run on every call, next to kernels of a few microseconds: each
+# looks a tensor's properties up once.
 def _quant_rows(name: str, cache: QuantCache, x: torch.Tensor, heads: int, dtype):
     """Strides (sequence, head, token) of rows [B, heads, n, 128]."""
-    if x.dim() != 4 or x.shape[0] != cache.B or x.shape[1] != heads or x.shape[3] != HEAD_DIM:
-        raise ValueError(f"{name} must be [{cache.B}, {heads}, n, {HEAD_DIM}], "
-                         f"not {list(x.shape)}")
+    sh = x.shape
+    if len(sh) != 4 or sh[0] != cache.B or sh[1] != heads or sh[3] != HEAD_DIM:
+        raise ValueError(f"{name} must be [{cache.B}, {heads}, n, {HEAD_DIM}], not {list(sh)}")
     if x.dtype != dtype or x.device != cache.device:
         raise ValueError(f"{name} must be {dtype} on {cache.device}, not {x.dtype} on {x.device}")
-    if x.stride(3) != 1 or x.shape[2] > 0 and min(x.stride()[:3]) < 0:
+    st = x.stride()
+    if st[3] != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
     # a dimension of one entry has no stride of its own
-    return tuple(x.stride(i) if x.shape[i] > 1 else 0 for i in range(3))
+    return (st[0] if sh[0] > 1 else 0, st[1] if sh[1] > 1 else 0, st[2] if sh[2] > 1 else 0)
+
+
+def _quant_written(name: str, x: torch.Tensor, st):
+    if 0 in st and any(n > 1 and s == 0 for n, s in zip(x.shape, st)):
+        raise ValueError(f"{name} is written: its rows may not overlap")
 
 
 def _quant_counts(name: str, cache: QuantCache, t: Optional[torch.Tensor]):
-    if t is not None and (t.dtype != torch.int32 or t.device != cache.device or
-                          t.shape != (cache.B,) or not t.is_contiguous()):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != cache.device or t.shape != (cache.B,) or \
+            not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 [{cache.B}] on {cache.device}")
-    return _ptr(t)
+    return t.data_ptr()
+
+
+def _quant_call(name: str, cache: QuantCache, stream, *args) -> None:
+    """Run an entry point on the cache's device, on `stream` or that device's
+    current stream."""
+    dev = cache.device
+    if dev.type != "cuda":
+        raise ValueError(f"the cache is on {dev}, not on a CUDA device")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the cache on {dev}")
+    else:
+        raw = stream.cuda_stream
+    fn = getattr(_lib, name)
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(cache.desc_ref, *args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(cache.desc_ref, *args, raw)
+    if rc != 0:
+        raise LrkvError(name, rc)
 
 
 def quant_append(cache: QuantCache, k: torch.Tensor, v: torch.Tensor,
@@ -487,11 +520,8 @@ def quant_append(cache: QuantCache, k: torch.Tensor, v: torch.Tensor,
     st = _quant_rows("k", cache, k, cache.H_kv, torch.bfloat16)
     if _quant_rows("v", cache, v, cache.H_kv, torch.bfloat16) != st or k.shape != v.shape:
         raise ValueError("k and v must have the same shape and strides")
-    counts = _quant_counts("n_new", cache, n_new)
-    with torch.cuda.device(cache.device):
-        _check("lrkv_quant_append", _lib.lrkv_quant_append(
-            ctypes.byref(cache.desc), _ptr(k), _ptr(v), k.shape[2], counts, *st,
-            _stream(stream)))
+    _quant_call("lrkv_quant_append", cache, stream, k.data_ptr(), v.data_ptr(), k.shape[2],
+                _quant_counts("n_new", cache, n_new), *st)
 
 
 def quant_read(cache: QuantCache, k: torch.Tensor, v: torch.Tensor,
@@ -499,18 +529,16 @@ def quant_read(cache: QuantCache, k: torch.Tensor, v: torch.Tensor,
     """lrkv_quant_read: write the values of tokens first[b] .. first[b] + n - 1
     (from token 0 when first is None) into k, v [B, H_kv, n, 128], fp32 or
     bf16; rows of tokens that do not exist are left as they were."""
-    if k.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"k must be bf16 or fp32, not {k.dtype}")
-    st = _quant_rows("k", cache, k, cache.H_kv, k.dtype)
-    if _quant_rows("v", cache, v, cache.H_kv, k.dtype) != st or k.shape != v.shape:
+    dtype = k.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float32:
+        raise ValueError(f"k must be bf16 or fp32, not {dtype}")
+    st = _quant_rows("k", cache, k, cache.H_kv, dtype)
+    if _quant_rows("v", cache, v, cache.H_kv, dtype) != st or k.shape != v.shape:
         raise ValueError("k and v must have the same shape and strides")
-    if any(n > 1 and s == 0 for n, s in zip(k.shape, st)):
-        raise ValueError("k and v are written: their rows may not overlap")
-    counts = _quant_counts("first", cache, first)
-    with torch.cuda.device(cache.device):
-        _check("lrkv_quant_read", _lib.lrkv_quant_read(
-            ctypes.byref(cache.desc), counts, k.shape[2], _ptr(k), _ptr(v),
-            _dtype_code(k.dtype), *st, _stream(stream)))
+    _quant_written("k", k, st)
+    _quant_call("lrkv_quant_read", cache, stream, _quant_counts("first", cache, first),
+                k.shape[2], k.data_ptr(), v.data_ptr(),
+                LRKV_F32 if dtype == torch.float32 else LRKV_BF16, *st)
     return k, v
 
 
@@ -518,8 +546,7 @@ def quant_attn_workspace(cache: QuantCache, num_q_heads: int, n_queries: int = 1
     """Zero-filled workspace for quant_attn calls of up to n_queries queries
     per sequence (the library keeps its counters at zero)."""
     with torch.cuda.device(cache.device):
-        n = int(_lib.lrkv_quant_attn_workspace_bytes(ctypes.byref(cache.desc), num_q_heads,
-                                                     n_queries))
+        n = int(_lib.lrkv_quant_attn_workspace_bytes(cache.desc_ref, num_q_heads, n_queries))
     if n == 0:
         raise LrkvError("lrkv_quant_attn_workspace_bytes", -2)
     return torch.zeros(n, dtype=torch.uint8, device=cache.device)
@@ -534,21 +561,20 @@ def quant_attn(cache: QuantCache, q: torch.Tensor, scale: float, o: torch.Tensor
     if o.shape != q.shape:
         raise ValueError("q and o must have the same shape")
     q4, o4 = (q.unsqueeze(2), o.unsqueeze(2)) if q.dim() == 3 else (q, o)
-    heads = q4.shape[1] if q4.dim() == 4 else 0
+    sh = q4.shape
+    heads = sh[1] if len(sh) == 4 else 0
     qst = _quant_rows("q", cache, q4, heads, torch.bfloat16)
     ost = _quant_rows("o", cache, o4, heads, torch.bfloat16)
-    if any(n > 1 and s == 0 for n, s in zip(o4.shape, ost)):
-        raise ValueError("o is written: its rows may not overlap")
-    if o.data_ptr() == q.data_ptr() and o.numel():
+    _quant_written("o", o4, ost)
+    qp, op = q4.data_ptr(), o4.data_ptr()
+    if qp == op and qp:
         raise ValueError("o may not be q: q is read while o is written")
     if workspace.device != cache.device or not workspace.is_contiguous() or \
             workspace.dtype != torch.uint8:
         raise ValueError(f"workspace must be contiguous uint8 on {cache.device}")
-    counts = _quant_counts("n_q", cache, n_q)
-    with torch.cuda.device(cache.device):
-        _check("lrkv_quant_attn", _lib.lrkv_quant_attn(
-            ctypes.byref(cache.desc), _ptr(q4), heads, q4.shape[2], counts, *qst, float(scale),
-            _ptr(o4), *ost, _ptr(workspace), workspace.numel(), _stream(stream)))
+    _quant_call("lrkv_quant_attn", cache, stream, qp, heads, sh[2],
+                _quant_counts("n_q", cache, n_q), *qst, scale, op, *ost, workspace.data_ptr(),
+                workspace.numel())
     return o
 
 

@@ -11,6 +11,13 @@ above and below the fraction bar, ds the error of a score (it scales the
 weight in both sums): 128 products added in fp32, at worst truncated,
 128 * 2^-23 of scale * sum |q k|, and 2^-21 of the score itself for its
 scaling and the exponential; 2^-20 for the few roundings of rescaling.
+
+And + 2^-38 L f: fp16 has a floor.  A weight p s_v is held times 2^13 / 2^M',
+where 2^M' <= the row's largest p s_v, so what is at least 2^13 there has a
+smallest step of 2^-24: each of L weights is off by at most 2^-25 2^-13 of the
+largest, times a code of at most 127 or 448: f = the largest p * (largest |v|
+of the token's block).  It shows where the one token that counts has code 0
+in a dim, and the row's result there is what tokens of 2^-30 its weight say.
 """
 import numpy as np
 import pytest
@@ -99,6 +106,7 @@ def _check_attention(lrkv, cache, oc, G, n, n_q=None, seed=9, token_major=False,
         ds = s2[b, :, :m, 0] * 128 * 2.0 ** -23 + s2[b, :, :m, 1] * 2.0 ** -21
         tol = 2.0 ** -8 * np.abs(ref[b, :, :m]) + w[b, :, :m] * (
             2.0 ** -11 + 2 * L * 2.0 ** -24 + 2 * ds + 2.0 ** -20)[..., None]
+        tol += (2.0 ** -38 * L * s2[b, :, :m, 2])[..., None]
         err = np.abs(got[b, :, :m] - ref[b, :, :m])
         assert not np.isnan(got[b, :, :m]).any(), b
         assert (err <= tol).all(), (b, np.max(err - tol), np.max(err / np.maximum(tol, 1e-30)))
