@@ -85,13 +85,14 @@ class QuantCacheOracle:
     def attend(self, q, scale: float, n_q=None):
         """o [B, H_q, n, 128] (NaN rows past a sequence's queries) and, for the
         tests' error bounds, w = sum p |v| of the same shape and
-        s [B, H_q, n, 3]: a row's largest sum |q k| * scale, its largest
-        |score| and its largest p * (largest |v| of the token's block)."""
+        s [B, H_q, n, 4]: a row's largest sum |q k| * scale, its largest
+        |score|, its largest p * (largest |v| of the token's block) and the
+        largest |v| it sees."""
         q = np.asarray(q, np.float64)
         B, Hq, n, _ = q.shape
         G = Hq // self.H
         o, w = np.full(q.shape, np.nan), np.zeros(q.shape)
-        s2 = np.zeros((B, Hq, n, 3))
+        s2 = np.zeros((B, Hq, n, 4))
         for b in range(B):
             L = self.length(b)
             m = n if n_q is None else int(np.clip(n_q[b], 0, n))
@@ -111,5 +112,6 @@ class QuantCacheOracle:
                         o[b, g, i] = p @ V[:seen]
                         w[b, g, i] = p @ np.abs(V[:seen])
                         s2[b, g, i] = (np.max(np.abs(K[:seen]) @ np.abs(q[b, g, i])) * scale,
-                                       np.max(np.abs(s)), np.max(p * top[:seen]))
+                                       np.max(np.abs(s)), np.max(p * top[:seen]),
+                                       np.max(np.abs(V[:seen])))
         return o, w, s2

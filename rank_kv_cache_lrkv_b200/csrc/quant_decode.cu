@@ -511,6 +511,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
             }
           l[2 * n + j] = sum;
         }
+      int bad = 64;  // first open token whose value row is not finite
 #pragma unroll
       for (int s4 = 0; s4 < 4; ++s4) {
         uint32_t ph[NT][2], pw[NT][2];
@@ -536,6 +537,13 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
                              ? *reinterpret_cast<const uint2*>(vt + tok * kHeadDim + 64 * hf + 8 * g +
                                                                4 * q2)
                              : make_uint2(0, 0);
+              // a weight of 0 must stay 0: such rows count through `bad`
+              uint2& w = v[k][hf];
+              const uint32_t big = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+              if (max(big >> 16, big & 0xffffu) >= 0x7f80u) {
+                bad = min(bad, tok);
+                w = make_uint2(0, 0);
+              }
             }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -553,6 +561,11 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
           }
         }
       }
+      bad = (int)__reduce_min_sync(0xffffffffu, (uint32_t)bad);
+      if (bad < 64)
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i)
+          if (base + bad <= pos[i]) l[i] = NAN;
     }
 
     // ---------------- combine the warps' (m, l, M', acc)
@@ -675,10 +688,12 @@ static int launch(const QuantAttnArgs& a, const DevInfo& info, cudaStream_t st) 
              : LRKV_ERR_CUDA;
 }
 
-size_t quant_attn_workspace(int, int, int, int) {
+size_t quant_attn_workspace(int, int H, int Hq, int n) {
   int dev = 0;
   DevInfo info;
-  return current_device_info(dev, info) == LRKV_OK ? dec_ws(info.sms) : 0;
+  if (current_device_info(dev, info) != LRKV_OK) return 0;
+  // the counters come first in both layouts, the records need no zeros
+  return (long long)n * (Hq / H) <= kMaxRows ? dec_ws(info.sms) : quant_prefill_workspace(info.sms);
 }
 
 int quant_attn_launch(const QuantAttnArgs& a, cudaStream_t st) {
@@ -688,7 +703,9 @@ int quant_attn_launch(const QuantAttnArgs& a, cudaStream_t st) {
   if (rc != LRKV_OK) return rc;
   if ((long long)a.n * a.G <= 8)
     return a.c.e4m3 ? launch<true, 1, 5, 2>(a, info, st) : launch<false, 1, 5, 2>(a, info, st);
-  return a.c.e4m3 ? launch<true, 2, 4, 2>(a, info, st) : launch<false, 2, 4, 2>(a, info, st);
+  if ((long long)a.n * a.G <= kMaxRows)
+    return a.c.e4m3 ? launch<true, 2, 4, 2>(a, info, st) : launch<false, 2, 4, 2>(a, info, st);
+  return quant_prefill_launch(a, info, st);
 }
 
 }  // namespace lrkv

@@ -1,0 +1,844 @@
+// Attention of many query rows over the 8-bit full-rank cache, on the
+// fifth-generation tensor cores.
+//
+// The mathematics is quant_decode.cu's: codes are exact fp16 numbers, q is
+// fp16 times a power of two per row, the blocks' scales stay outside the
+// products.  Row r of a unit (sequence, KV head) is query r / G of q head
+// h G + r % G, so the heads of a group share their keys' tiles.  A tile is
+// 256 rows, two groups of 128 (the MMA's M); a step is 128 keys (two pages).
+//
+// Persistent, one CTA per SM, 16 warps:
+//  * warps 0-3 and 4-7: softmax of group 0 and 1, one row per thread (its
+//    TMEM lane).  S comes from TMEM, P goes back over S's columns as fp16,
+//    and the two groups take turns with the tensor cores: while one is in
+//    its softmax, the other's products run.
+//  * warps 8-11: converters.  Codes from L2 into registers a step ahead, two
+//    bytes to two fp16 numbers, into the 128-byte-swizzled K-major tiles
+//    (keys as rows for Q K^T; the stored transpose of V is already K-major
+//    for P V).  The open block's bf16 rows become fp16 under a power of two.
+//  * warp 12, one lane: per step and group P V (A from TMEM) and then the
+//    next step's Q K^T.  A group's S barrier so tells that its O is at rest.
+// A row keeps its references m (scores) and M' (scores + floor(log2 s_v)) as
+// long as they lag by at most 2^kLazy, so O is seldom rescaled; a weight is
+// then at most 2^(1 + kLazy + kBoostLog) = 2^15 and fp16's floor lies 2^-33
+// below the row's largest.
+//
+// The steps of all tiles are laid end to end and each CTA takes an equal
+// contiguous range (causal tiles differ in length, and a few tiles over a
+// long cache still fill the GPU).  A tile cut by a range's border goes
+// through records in the workspace, folded in order by the last CTA to
+// arrive.
+#include "quant.cuh"
+#include "tcgen05.cuh"
+
+namespace lrkv {
+
+namespace {
+
+constexpr int kTileRows = 256;
+constexpr int kStepKeys = 128;
+constexpr int kPreThreads = 512;
+constexpr int kHalf = 128 * 128;                // bytes of 64 columns of 128 rows
+constexpr int kTileBytes = 2 * kHalf;           // a [128][128] fp16 tile
+constexpr int kScaleRing = 4;
+constexpr float kLazy = 6.f;
+constexpr float kBoostLog = 8.f;
+
+struct StepScales {
+  float sk[2], sv[2];
+  int ok[2];    // the page's tokens count
+  int minbad;   // first open token whose value row is not finite
+  int pad;
+};
+
+struct PrePlan {
+  int q, k, v, bars, scales, start, len, nq, sum, misc, total;
+};
+constexpr int kBars = 19;
+__host__ __device__ inline PrePlan pre_plan(int B) {
+  PrePlan p;
+  p.q = 0;
+  p.k = 2 * kTileBytes;
+  p.v = p.k + 2 * kTileBytes;
+  p.bars = p.v + 2 * kTileBytes;
+  p.scales = (p.bars + kBars * 8 + 15) / 16 * 16;
+  p.start = p.scales + kScaleRing * (int)sizeof(StepScales);
+  p.sum = p.start + (B + 1) * 8;
+  p.len = p.sum + B * 4;
+  p.nq = p.len + B * 4;
+  p.misc = p.nq + B * 4;
+  p.total = (p.misc + 64 + 15) / 16 * 16;
+  return p;
+}
+
+// Records: [2 per CTA][33][256] float4: (m, l, M', -) of a row, then its 128
+// sums four at a time, rows side by side.
+constexpr size_t kPreRecord = (size_t)33 * kTileRows;
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// fp16 A and B, fp32 D, M = 128, N = 128, both K-major.
+constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+
+#define LRKV_R32(v, o)                                                                          \
+  "=r"(v[o + 0]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]),               \
+      "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7]), "=r"(v[o + 8]), "=r"(v[o + 9]),           \
+      "=r"(v[o + 10]), "=r"(v[o + 11]), "=r"(v[o + 12]), "=r"(v[o + 13]), "=r"(v[o + 14]),      \
+      "=r"(v[o + 15]), "=r"(v[o + 16]), "=r"(v[o + 17]), "=r"(v[o + 18]), "=r"(v[o + 19]),      \
+      "=r"(v[o + 20]), "=r"(v[o + 21]), "=r"(v[o + 22]), "=r"(v[o + 23]), "=r"(v[o + 24]),      \
+      "=r"(v[o + 25]), "=r"(v[o + 26]), "=r"(v[o + 27]), "=r"(v[o + 28]), "=r"(v[o + 29]),      \
+      "=r"(v[o + 30]), "=r"(v[o + 31])
+// 32 consecutive columns of this thread's lane, no wait.
+template <int kOff, int N>
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[N]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : LRKV_R32(v, kOff)
+      : "r"(addr));
+}
+// Wait for this thread's loads; ties 32 of their registers to the wait.
+template <int kOff, int N>
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[kOff + i]));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+template <int R>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 add2(const float2 a, const float2 b) {
+  unsigned long long dd, aa, bb;
+  memcpy(&aa, &a, 8); memcpy(&bb, &b, 8);
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(dd) : "l"(aa), "l"(bb));
+  float2 d;
+  memcpy(&d, &dd, 8);
+  return d;
+}
+
+// A part of a tile: steps [j0, j1) of `steps` in this CTA's range, `first`
+// the line's index of its step 0; ntile[g]: steps that group g needs.
+struct PrePart {
+  int b, h, r0, steps, j0, j1, ntile[2];
+  long long first;
+};
+
+template <bool kE4M3>
+__global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttnArgs a, int RT) {
+  extern __shared__ __align__(1024) uint8_t sm_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  const QuantView& c = a.c;
+  const PrePlan pl = pre_plan(c.B);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + pl.bars);
+  uint64_t *kfull = bars, *kempty = bars + 2, *vfull = bars + 4, *vempty = bars + 6,
+           *qfull = bars + 8, *sfull = bars + 10, *pfull = bars + 12, *ofull = bars + 14,
+           *oempty = bars + 16, *mdone = bars + 18;
+  StepScales* scales = reinterpret_cast<StepScales*>(sm + pl.scales);
+  long long* start = reinterpret_cast<long long*>(sm + pl.start);
+  int* ssum = reinterpret_cast<int*>(sm + pl.sum);
+  int* slen = reinterpret_cast<int*>(sm + pl.len);
+  int* snq = reinterpret_cast<int*>(sm + pl.nq);
+  volatile int* fail = reinterpret_cast<volatile int*>(sm + pl.misc);
+  uint32_t* taddr = reinterpret_cast<uint32_t*>(sm + pl.misc + 4);
+  volatile int* lastflag = fail + 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    *fail = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kfull[i], 128);
+      mbar_init(&kempty[i], 1);
+      mbar_init(&vfull[i], 128);
+      mbar_init(&vempty[i], 1);
+      mbar_init(&qfull[i], 128);
+      mbar_init(&sfull[i], 2);  // the products' commit and the issuer itself
+      mbar_init(&pfull[i], 128);
+      mbar_init(&ofull[i], 1);
+      mbar_init(&oempty[i], 128);
+    }
+    mbar_init(mdone, 1);
+    mbar_fence_init();
+  }
+  pdl_trigger();
+  pdl_wait();
+  for (int b = tid; b < c.B; b += kPreThreads) {
+    slen[b] = quant_len(c, b);
+    snq[b] = quant_queries(a, b);
+    ssum[b] = 0;
+  }
+  if (warp == 12) {
+    tmem_alloc(taddr, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  // steps that group gr of row tile rt of sequence b needs
+  auto group_steps = [&](int b, int rt, int gr) {
+    const int R = snq[b] * a.G, lo_r = rt * kTileRows + gr * 128;
+    if (lo_r >= R) return 0;
+    const int maxpos = slen[b] - snq[b] + min(R - 1, lo_r + 127) / a.G;
+    return maxpos < 0 ? 0 : maxpos / kStepKeys + 1;
+  };
+  // steps of a tile: one at least for queries that see nothing (their zeros)
+  auto tile_steps = [&](int b, int rt) {
+    if (rt * kTileRows >= snq[b] * a.G) return 0;
+    return max(1, max(group_steps(b, rt, 0), group_steps(b, rt, 1)));
+  };
+  for (long long i = tid; i < (long long)c.B * RT; i += kPreThreads) {
+    const int b = (int)(i / RT), s = tile_steps(b, (int)(i - (long long)b * RT));
+    if (s) atomicAdd(&ssum[b], s);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int per = (c.B + 31) / 32, b0 = min(c.B, lane * per), b1 = min(c.B, b0 + per);
+    long long own = 0;
+    for (int b = b0; b < b1; ++b) own += (long long)ssum[b] * c.H;
+    long long incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    long long e = incl - own;
+    for (int b = b0; b < b1; ++b) {
+      start[b] = e;
+      e += (long long)ssum[b] * c.H;
+    }
+    if (lane == 31) start[c.B] = incl;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *taddr;
+  const long long total = start[c.B];
+  const int C = (int)min((long long)gridDim.x, total);
+  const bool works = (int)blockIdx.x < C;
+  const long long lo = works ? total * blockIdx.x / C : 0;
+  const long long hi = works ? total * (blockIdx.x + 1) / C : 0;
+
+  // the part that step x of the line belongs to (a whole warp calls)
+  auto part_of = [&](long long x) {
+    PrePart p;
+    int l = 0, r = c.B;
+    while (r - l > 1) {
+      const int mid = (l + r) >> 1;
+      if (start[mid] <= x) l = mid; else r = mid;
+    }
+    p.b = l;
+    const long long in = x - start[l];
+    p.h = (int)(in / ssum[l]);
+    int left = (int)(in - (long long)p.h * ssum[l]), rt = 0;
+    for (;; rt += 32) {
+      int s = tile_steps(l, rt + lane), incl = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, incl > left);
+      if (past) {
+        const int w = __ffs(past) - 1;
+        p.steps = __shfl_sync(0xffffffffu, s, w);
+        left -= __shfl_sync(0xffffffffu, incl, w) - p.steps;
+        rt += w;
+        break;
+      }
+      left -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    p.r0 = rt * kTileRows;
+    p.first = x - left;
+    p.j0 = left;  // x is the first of the range or the tile's first
+    p.j1 = (int)(min(hi, p.first + p.steps) - p.first);
+    p.ntile[0] = group_steps(l, rt, 0);
+    p.ntile[1] = group_steps(l, rt, 1);
+    return p;
+  };
+
+  if (warp < 8) {
+    // ================ softmax
+    regs_inc<192>();
+    const int gr = warp >> 2, row = tid & 127;  // TMEM lane = row of the group
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + gr * 128, tO = tmem + lane_base + 256 + gr * 128;
+    uint8_t* qs = sm + pl.q + gr * kTileBytes;
+    float4* records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.ws) + ((size_t)gridDim.x * 4 + 255) / 256 * 256);
+    int* counters = static_cast<int*>(a.ws);
+    uint32_t ns = 0, no = 0;  // S tiles and O sums seen
+    uint32_t done = 0;        // steps of the parts before
+    for (long long x = lo; x < hi;) {
+      const PrePart p = part_of(x);
+      const int L = slen[p.b], nq = snq[p.b], R = nq * a.G, pos0 = L - nq;
+      const int rr = p.r0 + gr * 128 + row;
+      const bool valid = rr < R;
+      const int pos = valid ? pos0 + rr / a.G : 0x7fffffff;
+      const int minpos = pos0 + (p.r0 + gr * 128) / a.G;
+      const int n = min(p.j1, p.ntile[gr]) - p.j0;  // this group's steps here
+      float m = -INFINITY, l = 0.f, mv = -INFINITY;
+      if (n > 0) {
+        // ---- the row of q: fp16, its largest element in [2^14, 2^15)
+        float fcol;
+        {
+          const float sgn = a.scale < 0.f ? -1.f : 1.f;
+          uint4 w[16];
+          const __nv_bfloat16* src = a.q + p.b * a.qs + (long long)(p.h * a.G + (valid ? rr % a.G : 0)) * a.qh +
+                                     (long long)(valid ? rr / a.G : 0) * a.qt;
+          uint32_t mx = 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            w[i] = valid ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+            mx = __vmaxu2(mx, w[i].x & 0x7fff7fffu);
+            mx = __vmaxu2(mx, w[i].y & 0x7fff7fffu);
+            mx = __vmaxu2(mx, w[i].z & 0x7fff7fffu);
+            mx = __vmaxu2(mx, w[i].w & 0x7fff7fffu);
+          }
+          mx = max(mx >> 16, mx & 0xffffu);
+          int e = (int)(mx >> 7) - 127;
+          e = mx == 0 || e == 128 ? 14 : max(e, -100);
+          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23) * sgn;
+          fcol = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * (fabsf(a.scale) * kLog2e);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint4 h = make_uint4(pack_h2(bf_lo(w[i].x) * up, bf_hi(w[i].x) * up),
+                                       pack_h2(bf_lo(w[i].y) * up, bf_hi(w[i].y) * up),
+                                       pack_h2(bf_lo(w[i].z) * up, bf_hi(w[i].z) * up),
+                                       pack_h2(bf_lo(w[i].w) * up, bf_hi(w[i].w) * up));
+            *reinterpret_cast<uint4*>(qs + (i >> 3) * kHalf + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = h;
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&qfull[gr]);
+        for (int i = 0; i < n; ++i) {
+          const int j = p.j0 + i, base = j * kStepKeys;
+          if (!tc_wait_warp(&sfull[gr], ns & 1, fail, lane)) break;
+          ++ns;
+          tc_fence_after();
+          uint32_t s[128];
+          tmem_ld32<0>(tS, s);
+          tmem_ld32<32>(tS + 32, s);
+          tmem_ld32<64>(tS + 64, s);
+          tmem_ld32<96>(tS + 96, s);
+          const StepScales sc = scales[(done + i) % kScaleRing];
+          float f[2], ev[2], fv[2], mx[2];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            f[hf] = fcol * sc.sk[hf];
+            const bool vnan = sc.sv[hf] != sc.sv[hf];
+            const uint32_t vb = __float_as_uint(sc.sv[hf]);
+            ev[hf] = vnan ? 0.f : (float)((int)(vb >> 23) - 127);
+            fv[hf] = vnan ? sc.sv[hf] : __uint_as_float((vb & 0x7fffffu) | 0x3f800000u);
+          }
+          tmem_wait_ld32<0>(s);
+          tmem_wait_ld32<32>(s);
+          tmem_wait_ld32<64>(s);
+          tmem_wait_ld32<96>(s);
+          // ---- what the row does not see
+          const bool edge = base + kStepKeys - 1 > minpos || !sc.ok[0] || !sc.ok[1];
+          if (edge) {
+            const int last0 = sc.ok[0] ? pos - base : -1, last1 = sc.ok[1] ? pos - base : -1;
+#pragma unroll
+            for (int k = 0; k < 128; ++k)
+              if (k > (k < 64 ? last0 : last1)) s[k] = 0xff800000u;
+          }
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 64; k += 4) {
+              x0 = fmaxf(x0, fmaxf(__uint_as_float(s[64 * hf + k]), __uint_as_float(s[64 * hf + k + 1])));
+              x1 = fmaxf(x1, fmaxf(__uint_as_float(s[64 * hf + k + 2]), __uint_as_float(s[64 * hf + k + 3])));
+            }
+            x0 = fmaxf(x0, x1);
+            mx[hf] = x0 == -INFINITY ? x0 : x0 * f[hf];  // f >= 0
+          }
+          const float mn = fmaxf(mx[0], mx[1]), vn = fmaxf(mx[0] + ev[0], mx[1] + ev[1]);
+          if (mn > m + kLazy) {  // also from -inf
+            l *= ex2_approx(m - mn);
+            m = mn;
+          }
+          const bool grow = vn > mv + kLazy;
+          if (__any_sync(0xffffffffu, grow) && i > 0) {
+            const float cr = grow ? ex2_approx(mv - vn) : 1.f;
+#pragma unroll
+            for (int q4 = 0; q4 < 8; ++q4) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16 * q4, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * cr);
+              tmem_st16(tO + 16 * q4, o);
+            }
+          }
+          if (grow) mv = vn;
+          const float ref = m == -INFINITY ? 0.f : m, vref = mv == -INFINITY ? 0.f : mv;
+          const float2 nref = make_float2(-ref, -ref);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            // 2^(m - M') s_v 2^kBoostLog (no more than 2^126: p is 0 there)
+            const float wm = fv[hf] * ex2_approx(fminf(ref + ev[hf] - vref, 112.f) + kBoostLog);
+            const float2 w2 = make_float2(wm, wm), f2 = make_float2(f[hf], f[hf]);
+#pragma unroll
+            for (int q4 = 0; q4 < 2; ++q4) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int k = 64 * hf + 32 * q4 + 2 * e;
+                float2 v = nref;
+                fma2(v, make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f2);
+                v.x = ex2_approx(v.x);
+                v.y = ex2_approx(v.y);
+                if (edge) {  // a NaN scale does not reach what is not seen
+                  if (s[k] == 0xff800000u) v.x = 0.f;
+                  if (s[k + 1] == 0xff800000u) v.y = 0.f;
+                }
+                sum = add2(sum, v);
+                float2 w = mul2(v, w2);
+                if (edge) {
+                  if (s[k] == 0xff800000u) w.x = 0.f;
+                  if (s[k + 1] == 0xff800000u) w.y = 0.f;
+                }
+                pk[e] = pack_h2(w.x, w.y);
+              }
+              tmem_st16(tS + 32 * hf + 16 * q4, pk);
+            }
+          }
+          l += sum.x + sum.y;
+          if (sc.minbad <= pos && valid) l = NAN;  // a value row that is not finite is seen
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&pfull[gr]);
+        }
+      }
+      // ---- the row's sums
+      const bool whole = p.j0 == 0 && p.j1 == p.steps;
+      const float4 st = make_float4(m, l, mv, 0.f);
+      __nv_bfloat16* dst = a.o + p.b * a.os + (long long)(p.h * a.G + (valid ? rr % a.G : 0)) * a.oh +
+                           (long long)(valid ? rr / a.G : 0) * a.ot;
+      float4* rec = records + ((size_t)2 * blockIdx.x + (p.j0 == 0 ? 1 : 0)) * kPreRecord + gr * 128 + row;
+      const float fin = whole ? (l == 0.f ? 0.f : ex2_approx(mv - m - kBoostLog) / l) : 1.f;
+      if (n > 0) {
+        tc_wait_warp(&ofull[gr], no & 1, fail, lane);
+        ++no;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32<0>(tO + 32 * q4, o);
+          tmem_wait_ld32<0>(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (whole) {
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack_bf16x2(l == 0.f ? 0.f : __uint_as_float(o[8 * e + 2 * k]) * fin,
+                                   l == 0.f ? 0.f : __uint_as_float(o[8 * e + 2 * k + 1]) * fin);
+              *reinterpret_cast<uint4*>(dst + 32 * q4 + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            rec[(size_t)(1 + 8 * q4 + e) * kTileRows] =
+                make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+        }
+      }
+      if (n > 0) {
+        tc_fence_before();
+        mbar_arrive(&oempty[gr]);
+      }
+      if (!whole) {
+        rec[0] = st;
+        const int c0 = (int)(((p.first + 1) * C - 1) / total);
+        const int c1 = (int)(((p.first + p.steps) * C - 1) / total);
+        __threadfence();
+        named_bar(1, 256);
+        if (tid == 0) {
+          const int before = atomicAdd(&counters[c0], 1);
+          *lastflag = before == c1 - c0;
+          if (before == c1 - c0) counters[c0] = 0;
+        }
+        named_bar(1, 256);
+        const bool last = *lastflag != 0;
+        named_bar(1, 256);  // read before the next part writes it
+        if (last && valid) {
+          __threadfence();
+          auto part = [&](int cc) {
+            return records + ((size_t)2 * cc + (cc == c0 ? 1 : 0)) * kPreRecord + gr * 128 + row;
+          };
+          float M = -INFINITY, ls = 0.f, Z = -INFINITY;
+          for (int cc = c0; cc <= c1; ++cc) {
+            const float4 t = __ldcg(part(cc));
+            if (t.x == -INFINITY && t.y == 0.f) continue;
+            const float mn = fmaxf(M, t.x), mr = mn == -INFINITY ? 0.f : mn;
+            ls = ls * ex2_approx(M - mr) + t.y * ex2_approx(t.x - mr);
+            M = mn;
+            Z = fmaxf(Z, t.z);
+          }
+          const float zr = Z == -INFINITY ? 0.f : Z;
+          const float ff = ls == 0.f ? 0.f : ex2_approx(Z - M - kBoostLog) / ls;
+          for (int q8 = 0; q8 < 16; ++q8) {
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = 0.f;
+            for (int cc = c0; cc <= c1; ++cc) {
+              const float4* t = part(cc);
+              const float4 stt = __ldcg(t);
+              if (stt.x == -INFINITY && stt.y == 0.f) continue;
+              const float fz = ex2_approx(stt.z - zr);
+              const float4 u = __ldcg(t + (size_t)(1 + 2 * q8) * kTileRows);
+              const float4 v = __ldcg(t + (size_t)(2 + 2 * q8) * kTileRows);
+              o[0] += u.x * fz; o[1] += u.y * fz; o[2] += u.z * fz; o[3] += u.w * fz;
+              o[4] += v.x * fz; o[5] += v.y * fz; o[6] += v.z * fz; o[7] += v.w * fz;
+            }
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_bf16x2(ls == 0.f ? 0.f : o[2 * k] * ff, ls == 0.f ? 0.f : o[2 * k + 1] * ff);
+            *reinterpret_cast<uint4*>(dst + 8 * q8) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      done += max(0, min(p.j1, max(p.ntile[0], p.ntile[1])) - p.j0);
+      x = p.first + p.j1;
+    }
+  } else if (warp < 12) {
+    // ================ converters
+    regs_dec<96>();
+    const int ct = tid - 256;
+    const int sub = ct >> 2, ch = ct & 3;  // 32 rows x 4 chunks a round
+    uint4 kr[8], vr[8];
+    uint32_t cnt = 0;  // steps converted
+    const uint8_t* slab[2];
+    float2 nsc[2];  // their scales
+    // slabs of step j (nullptr: open, past the end or out of range)
+    auto pages = [&](const PrePart& p, int j, const uint8_t* (&s)[2]) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int pg = 2 * j + u;
+        s[u] = nullptr;
+        if ((pg + 1) * kQBlock <= slen[p.b]) {
+          s[u] = quant_slab(c, p.b, p.h, pg);
+          if (s[u]) nsc[u] = __ldg(reinterpret_cast<const float2*>(s[u] + 2 * kQSide));
+          else if (ct == 0) quant_error(c, kErrBadPage);
+        }
+      }
+    };
+    // keys: token 32 i + sub of the page, chunks ch and ch + 4 (i = 0, 1)
+    auto load_k = [&](const uint8_t* (&s)[2]) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          kr[4 * u + i] = s[u] ? __ldg(reinterpret_cast<const uint4*>(
+                                     s[u] + quant_k_chunk(32 * (i >> 1) + sub, ch + 4 * (i & 1))))
+                               : make_uint4(0, 0, 0, 0);
+    };
+    auto load_v = [&](const uint8_t* (&s)[2]) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          vr[4 * u + i] = s[u] ? __ldg(reinterpret_cast<const uint4*>(s[u] + kQSide + (32 * i + sub) * kQBlock + ch * 16))
+                               : make_uint4(0, 0, 0, 0);
+    };
+    // 16 codes -> 32 bytes of fp16 at chunks cc, cc + 1 of a swizzled row
+    auto put = [&](uint8_t* rowp, int row, int cc, const uint4& w) {
+      uint32_t h[8];
+      quant_half4<kE4M3>(w.x, h[0], h[1]);
+      quant_half4<kE4M3>(w.y, h[2], h[3]);
+      quant_half4<kE4M3>(w.z, h[4], h[5]);
+      quant_half4<kE4M3>(w.w, h[6], h[7]);
+      *reinterpret_cast<uint4*>(rowp + ((cc ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(rowp + (((cc + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+    };
+    // Largest finite |x| (bf16 bits) of the open block's nt rows of one side
+    // and the first row that is not all finite (64: none).  Every warp looks
+    // at all of them: no barrier among warps that a failed wait may part.
+    auto scan_open = [&](const __nv_bfloat16* rows, int nt, int& bad) {
+      uint32_t mx = 0;
+      int fb = 64;
+#pragma unroll 4
+      for (int i = 0; i < 32; ++i) {
+        const int t = 2 * i + (lane >> 4);
+        if (t < nt) {
+          const uint4 w = *(reinterpret_cast<const uint4*>(rows + t * kHeadDim) + (lane & 15));
+          const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int hl = 0; hl < 2; ++hl) {
+              const uint32_t x = (e[q] >> (16 * hl)) & 0x7fffu;
+              if (x < 0x7f80u) mx = max(mx, x); else fb = min(fb, t);
+            }
+        }
+      }
+      bad = (int)__reduce_min_sync(0xffffffffu, (uint32_t)fb);
+      return __reduce_max_sync(0xffffffffu, mx);
+    };
+    bool live = true;
+    for (long long x = lo; x < hi && live;) {
+      const PrePart p = part_of(x);
+      const int L = slen[p.b], last = max(p.ntile[0], p.ntile[1]);
+      const int j1 = min(p.j1, last);
+      if (p.j0 < j1) {
+        pages(p, p.j0, slab);
+        load_k(slab);
+      }
+      for (int j = p.j0; j < j1; ++j) {
+        const int buf = cnt & 1;
+        uint8_t* kb = sm + pl.k + buf * kTileBytes;
+        uint8_t* vb = sm + pl.v + buf * kTileBytes;
+        load_v(slab);
+        // the scales; the open block among the two pages, if any
+        int open = -1;
+        float sk[2] = {1.f, 1.f}, sv[2] = {1.f, 1.f};
+        int ok[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int pg = 2 * j + u;
+          ok[u] = slab[u] != nullptr;
+          if (slab[u]) {
+            sk[u] = nsc[u].x;
+            sv[u] = nsc[u].y;
+          } else if (pg * kQBlock < L && (pg + 1) * kQBlock > L) {
+            open = u;
+            ok[u] = 1;
+          }
+        }
+        if (cnt >= 2 && !tc_wait_warp(&kempty[buf], ((cnt >> 1) - 1) & 1, fail, lane)) { live = false; break; }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 64 * u + 32 * (i >> 1) + sub;
+            if (u != open)
+              put(kb + (i & 1) * kHalf + row * 128, row, 2 * ch, kr[4 * u + i]);
+          }
+        int minbad = 0x7fffffff;
+        if (open >= 0) {
+          // keys of the open block: thread = (token, half of the dims)
+          const int pg = 2 * j + open, tok = ct >> 1, side = ct & 1, row = 64 * open + tok;
+          const int nt = L - pg * kQBlock;
+          int bad;
+          int e = (int)(scan_open(quant_tail(c, p.b, p.h, 0, pg * kQBlock), nt, bad) >> 7) - 127;
+          e = max(e, -100);
+          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+          sk[open] = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+          const uint4* src = reinterpret_cast<const uint4*>(quant_tail(c, p.b, p.h, 0, pg * kQBlock + tok)) + 8 * side;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 w = tok < nt ? src[i] : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(kb + side * kHalf + row * 128 + ((i ^ (row & 7)) << 4)) =
+                make_uint4(pack_h2(bf_lo(w.x) * up, bf_hi(w.x) * up),
+                           pack_h2(bf_lo(w.y) * up, bf_hi(w.y) * up),
+                           pack_h2(bf_lo(w.z) * up, bf_hi(w.z) * up),
+                           pack_h2(bf_lo(w.w) * up, bf_hi(w.w) * up));
+          }
+          const int ve = (int)(scan_open(quant_tail(c, p.b, p.h, 1, pg * kQBlock), nt, bad) >> 7) - 127;
+          if (bad < 64) minbad = pg * kQBlock + bad;
+          sv[open] = __uint_as_float((uint32_t)(127 - 7 + max(ve, -100)) << 23);
+        }
+        if (ct == 0) {
+          StepScales* s = &scales[cnt % kScaleRing];
+          s->sk[0] = sk[0]; s->sk[1] = sk[1];
+          s->sv[0] = sv[0]; s->sv[1] = sv[1];
+          s->ok[0] = ok[0]; s->ok[1] = ok[1];
+          s->minbad = minbad;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&kfull[buf]);
+        if (j + 1 < j1) {
+          pages(p, j + 1, slab);
+          load_k(slab);
+        }
+        if (cnt >= 2 && !tc_wait_warp(&vempty[buf], ((cnt >> 1) - 1) & 1, fail, lane)) { live = false; break; }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 32 * i + sub;
+            if (u != open) put(vb + u * kHalf + row * 128, row, 2 * ch, vr[4 * u + i]);
+          }
+        if (open >= 0) {
+          const int pg = 2 * j + open, row = ct;
+          const __nv_bfloat16* vt = quant_tail(c, p.b, p.h, 1, pg * kQBlock) + ct;
+          const int nt = L - pg * kQBlock;
+          const float down = sv[open];
+          const float up = __uint_as_float((254u << 23) - __float_as_uint(down));  // 1 / a power of two
+#pragma unroll 1
+          for (int cc = 0; cc < 8; ++cc) {
+            uint32_t h[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float v[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int t = 8 * cc + 2 * q + e;
+                v[e] = t < nt ? __bfloat162float(vt[t * kHeadDim]) * up : 0.f;
+                if (!(fabsf(v[e]) < 1e30f)) v[e] = 0.f;  // reported by minbad
+              }
+              h[q] = pack_h2(v[0], v[1]);
+            }
+            *reinterpret_cast<uint4*>(vb + open * kHalf + row * 128 + ((cc ^ (row & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&vfull[buf]);
+        ++cnt;
+      }
+      x = p.first + p.j1;
+    }
+  } else {
+    // ================ products
+    regs_dec<32>();
+    if (warp == 12) {
+      const uint32_t q0 = smem_u32(sm + pl.q), k0 = smem_u32(sm + pl.k), v0 = smem_u32(sm + pl.v);
+      uint32_t cnt = 0, nqf[2] = {0, 0}, np[2] = {0, 0}, nso[2] = {0, 0};
+      bool live = true;
+      for (long long x = lo; x < hi && live;) {
+        const PrePart p = part_of(x);
+        const int j1 = min(p.j1, max(p.ntile[0], p.ntile[1]));
+        // S of group gr, step j (its keys are in buffer `buf`)
+        auto scores = [&](int gr, int buf) {
+          if (lane == 0) {
+            tc_fence_after();
+            const uint32_t d = tmem + gr * 128, qa = q0 + gr * kTileBytes, kb = k0 + buf * kTileBytes;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+              tc_mma(d, sw128_desc(qa + off), sw128_desc(kb + off), kIdesc, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(&sfull[gr]);
+            mbar_arrive(&sfull[gr]);
+          }
+          __syncwarp();
+        };
+        auto active = [&](int gr, int j) { return j < min(p.j1, p.ntile[gr]); };
+        if (p.j0 < j1) {
+          const int buf = cnt & 1;
+          if (!tc_wait_warp(&kfull[buf], (cnt >> 1) & 1, fail, lane)) { live = false; break; }
+          for (int gr = 0; gr < 2 && live; ++gr)
+            if (active(gr, p.j0)) {
+              live = tc_wait_warp(&qfull[gr], nqf[gr] & 1, fail, lane);
+              ++nqf[gr];
+              if (live) scores(gr, buf);
+            }
+          if (!live) break;
+          if (lane == 0) tc_commit(&kempty[buf]);
+          __syncwarp();
+        }
+        for (int j = p.j0; j < j1 && live; ++j, ++cnt) {
+          const int buf = cnt & 1, nbuf = buf ^ 1;
+          if (!tc_wait_warp(&vfull[buf], (cnt >> 1) & 1, fail, lane)) { live = false; break; }
+          bool more = false;
+          for (int gr = 0; gr < 2 && live; ++gr) {
+            if (!active(gr, j)) continue;
+            if (!tc_wait_warp(&pfull[gr], np[gr] & 1, fail, lane)) { live = false; break; }
+            ++np[gr];
+            if (j == p.j0) {  // O's last sums have been read
+              if (nso[gr] > 0 && !tc_wait_warp(&oempty[gr], (nso[gr] - 1) & 1, fail, lane)) { live = false; break; }
+              ++nso[gr];
+            }
+            if (lane == 0) {
+              tc_fence_after();
+              const uint32_t d = tmem + 256 + gr * 128, pa = tmem + gr * 128, vb = v0 + buf * kTileBytes;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ts(d, pa + 8 * kk, sw128_desc(vb + (kk >> 2) * kHalf + (kk & 3) * 32), kIdesc,
+                       j > p.j0 || kk > 0 ? 1u : 0u);
+            }
+            __syncwarp();
+            if (active(gr, j + 1)) {
+              if (!more && !tc_wait_warp(&kfull[nbuf], ((cnt + 1) >> 1) & 1, fail, lane)) { live = false; break; }
+              more = true;
+              scores(gr, nbuf);
+            } else {
+              if (lane == 0) tc_commit(&ofull[gr]);
+              __syncwarp();
+            }
+          }
+          if (!live) break;
+          if (lane == 0) {
+            tc_commit(&vempty[buf]);
+            if (more) tc_commit(&kempty[nbuf]);
+          }
+          __syncwarp();
+        }
+        x = p.first + p.j1;
+      }
+      // every product has ended before TMEM is freed
+      if (lane == 0 && works) {
+        tc_commit(mdone);
+        const uint64_t t0 = global_ns();
+        while (!mbar_try_wait(mdone, 0) && global_ns() - t0 < kTcTimeoutNs) {
+        }
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (tid == 0 && *fail) quant_error(c, kErrTimeout);
+}
+
+}  // namespace
+
+size_t quant_prefill_workspace(int C) {
+  return ((size_t)C * 4 + 255) / 256 * 256 + (size_t)C * 2 * kPreRecord * 16;
+}
+
+int quant_prefill_launch(const QuantAttnArgs& a, const DevInfo& info, cudaStream_t st) {
+  const void* fn = a.c.e4m3 ? (const void*)quant_prefill_kernel<true>
+                            : (const void*)quant_prefill_kernel<false>;
+  const int smem = pre_plan(a.c.B).total + 1024;
+  if (smem > info.optin) return LRKV_ERR_UNSUPPORTED;
+  const int rc = prepare_kernel(fn, true);
+  if (rc != LRKV_OK) return rc;
+  QuantAttnArgs args = a;
+  int RT = (int)(((long long)a.n * a.G + kTileRows - 1) / kTileRows);
+  void* p[] = {&args, &RT};
+  return launch_pdl(fn, dim3(info.sms), dim3(kPreThreads), smem, st, p) == cudaSuccess
+             ? LRKV_OK
+             : LRKV_ERR_CUDA;
+}
+
+}  // namespace lrkv

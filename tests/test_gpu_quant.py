@@ -12,12 +12,17 @@ weight in both sums): 128 products added in fp32, at worst truncated,
 128 * 2^-23 of scale * sum |q k|, and 2^-21 of the score itself for its
 scaling and the exponential; 2^-20 for the few roundings of rescaling.
 
-And + 2^-38 L f: fp16 has a floor.  A weight p s_v is held times 2^13 / 2^M',
-where 2^M' <= the row's largest p s_v, so what is at least 2^13 there has a
-smallest step of 2^-24: each of L weights is off by at most 2^-25 2^-13 of the
-largest, times a code of at most 127 or 448: f = the largest p * (largest |v|
-of the token's block).  It shows where the one token that counts has code 0
+And + 2^-(25 + b) L f: fp16 has a floor.  A weight p s_v is held times 2^b /
+2^M', where 2^M' <= the row's largest p s_v, b = 13 for calls of at most 16
+rows a KV head and 8 above; fp16's smallest step is 2^-24, so each of L weights
+is off by at most 2^-25 2^-b of the largest, times a code of at most 127 or
+448: f = the largest p * (largest |v| of the token's block).  It shows where the one token that counts has code 0
 in a dim, and the row's result there is what tokens of 2^-30 its weight say.
+
+And + 2^-112 L max |v|: so does fp32.  2^(score - m) and the block's factor
+2^(m + log2 s_v - M'), cut at 2^112, are separate fp32 numbers; the cut and the
+flush of the first at 2^-126 only touch tokens whose p is under 2^-112, and
+make their weights smaller.  It shows where a block of zeros takes p ~ 1.
 """
 import numpy as np
 import pytest
@@ -106,7 +111,8 @@ def _check_attention(lrkv, cache, oc, G, n, n_q=None, seed=9, token_major=False,
         ds = s2[b, :, :m, 0] * 128 * 2.0 ** -23 + s2[b, :, :m, 1] * 2.0 ** -21
         tol = 2.0 ** -8 * np.abs(ref[b, :, :m]) + w[b, :, :m] * (
             2.0 ** -11 + 2 * L * 2.0 ** -24 + 2 * ds + 2.0 ** -20)[..., None]
-        tol += (2.0 ** -38 * L * s2[b, :, :m, 2])[..., None]
+        tol += (2.0 ** (-38 if n * G <= 16 else -33) * L * s2[b, :, :m, 2]
+                + 2.0 ** -112 * L * s2[b, :, :m, 3])[..., None]
         err = np.abs(got[b, :, :m] - ref[b, :, :m])
         assert not np.isnan(got[b, :, :m]).any(), b
         assert (err <= tol).all(), (b, np.max(err - tol), np.max(err / np.maximum(tol, 1e-30)))
@@ -384,6 +390,32 @@ def test_blocks_of_nan_show_where_they_are_seen(lrkv):
             assert not nan[0, 2:].any()
             for i in range(n):
                 assert bool(nan[0, :2, i].all() if L - n + i >= 128 else not nan[0, :2, i].any())
+
+
+def test_open_tokens_that_are_not_finite(lrkv):
+    """An open token's NaN or infinity among its values, or a NaN among its
+    keys, makes NaN of the queries that see it; earlier ones stay exact."""
+    B, H, L, n = 1, 2, 150, 24
+    clean, oc = _filled(lrkv, B, H, [L], "int8", seed=0, perm=False)
+    q = _rows(3, B, 4, n).cuda()
+    ref, _, _ = oc.attend(q.double().cpu().numpy(), SCALE)
+    for side, what in ((0, "nan"), (1, "nan"), (1, "inf")):
+        x = [_rows(1, B, H, L), _rows(2, B, H, L)]
+        x[side][0, 0, 140, 7] = float(what)
+        cache = lrkv.QuantCache(B, H, L)
+        lrkv.quant_append(cache, x[0].cuda(), x[1].cuda())
+        for m in (n, 2, 12):   # the last m queries, in calls of either kind
+            qm = q[:, :, n - m:].contiguous()
+            o = torch.zeros_like(qm)
+            lrkv.quant_attn(cache, qm, SCALE, o, lrkv.quant_attn_workspace(cache, 4, m))
+            for i in range(m):
+                sees = L - m + i >= 140
+                assert bool(torch.isnan(o[0, :2, i]).all()) == sees, (side, what, m, i)
+                assert not torch.isnan(o[0, 2:, i]).any()
+                for h in range(4):
+                    if h >= 2 or not sees:
+                        err = np.abs(o[0, h, i].double().cpu().numpy() - ref[0, h, n - m + i])
+                        assert err.max() < 2e-2
 
 
 def test_garbage_past_the_end_does_not_count(lrkv):
