@@ -28,6 +28,8 @@
 // long cache still fill the GPU).  A tile cut by a range's border goes
 // through records in the workspace, folded in order by the last CTA to
 // arrive.
+#include <type_traits>
+
 #include "quant.cuh"
 #include "tcgen05.cuh"
 
@@ -86,6 +88,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t bde
 // fp16 A and B, fp32 D, M = 128, N = 128, both K-major.
 constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r));
+  return r != 0;
+}
 #define LRKV_R32(v, o)                                                                          \
   "=r"(v[o + 0]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]),               \
       "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7]), "=r"(v[o + 8]), "=r"(v[o + 9]),           \
@@ -119,6 +128,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -145,10 +160,11 @@ __device__ __forceinline__ float2 add2(const float2 a, const float2 b) {
 }
 
 // A part of a tile: steps [j0, j1) of `steps` in this CTA's range, `first`
-// the line's index of its step 0; ntile[g]: steps that group g needs.
+// the line's index of its step 0; ntile(g): steps that group g needs.
 struct PrePart {
-  int b, h, r0, steps, j0, j1, ntile[2];
+  int b, h, r0, steps, j0, j1, nt0, nt1;
   long long first;
+  __device__ __forceinline__ int ntile(int g) const { return g ? nt1 : nt0; }
 };
 
 template <bool kE4M3>
@@ -277,31 +293,32 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     p.first = x - left;
     p.j0 = left;  // x is the first of the range or the tile's first
     p.j1 = (int)(min(hi, p.first + p.steps) - p.first);
-    p.ntile[0] = group_steps(l, rt, 0);
-    p.ntile[1] = group_steps(l, rt, 1);
+    p.nt0 = group_steps(l, rt, 0);
+    p.nt1 = group_steps(l, rt, 1);
     return p;
   };
 
   if (warp < 8) {
     // ================ softmax
-    regs_inc<192>();
+    regs_inc<152>();  // of 4 x 128 registers: 152 + 152 + 128 + 80
     const int gr = warp >> 2, row = tid & 127;  // TMEM lane = row of the group
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + gr * 128, tO = tmem + lane_base + 256 + gr * 128;
     uint8_t* qs = sm + pl.q + gr * kTileBytes;
-    float4* records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.ws) + ((size_t)gridDim.x * 4 + 255) / 256 * 256);
-    int* counters = static_cast<int*>(a.ws);
     uint32_t ns = 0, no = 0;  // S tiles and O sums seen
     uint32_t done = 0;        // steps of the parts before
     for (long long x = lo; x < hi;) {
-      const PrePart p = part_of(x);
-      const int L = slen[p.b], nq = snq[p.b], R = nq * a.G, pos0 = L - nq;
-      const int rr = p.r0 + gr * 128 + row;
-      const bool valid = rr < R;
-      const int pos = valid ? pos0 + rr / a.G : 0x7fffffff;
-      const int minpos = pos0 + (p.r0 + gr * 128) / a.G;
-      const int n = min(p.j1, p.ntile[gr]) - p.j0;  // this group's steps here
       float m = -INFINITY, l = 0.f, mv = -INFINITY;
+      int n;  // this group's steps here
+      {
+        const PrePart p = part_of(x);
+        const int nq = snq[p.b], pos0 = slen[p.b] - nq;
+        const int rr = p.r0 + gr * 128 + row;
+        const bool valid = rr < nq * a.G;
+        const int pos = valid ? pos0 + rr / a.G : 0x7fffffff;
+        const int minpos = pos0 + (p.r0 + gr * 128) / a.G;
+        n = min(p.j1, p.ntile(gr)) - p.j0;
+        const uint32_t steps = max(0, min(p.j1, max(p.nt0, p.nt1)) - p.j0);
       if (n > 0) {
         // ---- the row of q: fp16, its largest element in [2^14, 2^15)
         float fcol;
@@ -336,107 +353,137 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         fence_proxy_async_smem();
         mbar_arrive(&qfull[gr]);
         for (int i = 0; i < n; ++i) {
-          const int j = p.j0 + i, base = j * kStepKeys;
+          const int base = (p.j0 + i) * kStepKeys;
           if (!tc_wait_warp(&sfull[gr], ns & 1, fail, lane)) break;
           ++ns;
           tc_fence_after();
-          uint32_t s[128];
+          // the second half of S stays in registers between the maximum and
+          // the weights, the first is read again (128 registers a thread)
+          uint32_t s[64];
           tmem_ld32<0>(tS, s);
           tmem_ld32<32>(tS + 32, s);
-          tmem_ld32<64>(tS + 64, s);
-          tmem_ld32<96>(tS + 96, s);
-          const StepScales sc = scales[(done + i) % kScaleRing];
-          float f[2], ev[2], fv[2], mx[2];
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            f[hf] = fcol * sc.sk[hf];
-            const bool vnan = sc.sv[hf] != sc.sv[hf];
-            const uint32_t vb = __float_as_uint(sc.sv[hf]);
-            ev[hf] = vnan ? 0.f : (float)((int)(vb >> 23) - 127);
-            fv[hf] = vnan ? sc.sv[hf] : __uint_as_float((vb & 0x7fffffu) | 0x3f800000u);
-          }
-          tmem_wait_ld32<0>(s);
-          tmem_wait_ld32<32>(s);
-          tmem_wait_ld32<64>(s);
-          tmem_wait_ld32<96>(s);
-          // ---- what the row does not see
+          const StepScales& sc = scales[(done + i) % kScaleRing];
+          // s_v = 2^ev fv, 1 <= fv < 2 (a NaN stays in fv)
+          auto v_exp = [&](int hf) {
+            const float sv = sc.sv[hf];
+            return sv != sv ? 0.f : (float)((int)(__float_as_uint(sv) >> 23) - 127);
+          };
+          auto v_frac = [&](int hf) {
+            const float sv = sc.sv[hf];
+            return sv != sv ? sv : __uint_as_float((__float_as_uint(sv) & 0x7fffffu) | 0x3f800000u);
+          };
+          float mx[2];
           const bool edge = base + kStepKeys - 1 > minpos || !sc.ok[0] || !sc.ok[1];
-          if (edge) {
-            const int last0 = sc.ok[0] ? pos - base : -1, last1 = sc.ok[1] ? pos - base : -1;
+          // two bodies: masks cost every element two instructions and more
+          auto weigh = [&](auto edge_c) {
+            constexpr bool kEdge = decltype(edge_c)::value;
+            // what the row does not see of half hf
+            auto mask = [&](int hf) {
+              if constexpr (kEdge) {
+                const int last = sc.ok[hf] ? pos - base - 64 * hf : -1;
 #pragma unroll
-            for (int k = 0; k < 128; ++k)
-              if (k > (k < 64 ? last0 : last1)) s[k] = 0xff800000u;
-          }
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 64; k += 4) {
-              x0 = fmaxf(x0, fmaxf(__uint_as_float(s[64 * hf + k]), __uint_as_float(s[64 * hf + k + 1])));
-              x1 = fmaxf(x1, fmaxf(__uint_as_float(s[64 * hf + k + 2]), __uint_as_float(s[64 * hf + k + 3])));
-            }
-            x0 = fmaxf(x0, x1);
-            mx[hf] = x0 == -INFINITY ? x0 : x0 * f[hf];  // f >= 0
-          }
-          const float mn = fmaxf(mx[0], mx[1]), vn = fmaxf(mx[0] + ev[0], mx[1] + ev[1]);
-          if (mn > m + kLazy) {  // also from -inf
-            l *= ex2_approx(m - mn);
-            m = mn;
-          }
-          const bool grow = vn > mv + kLazy;
-          if (__any_sync(0xffffffffu, grow) && i > 0) {
-            const float cr = grow ? ex2_approx(mv - vn) : 1.f;
-#pragma unroll
-            for (int q4 = 0; q4 < 8; ++q4) {
-              uint32_t o[16];
-              tmem_ld16(tO + 16 * q4, o);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * cr);
-              tmem_st16(tO + 16 * q4, o);
-            }
-          }
-          if (grow) mv = vn;
-          const float ref = m == -INFINITY ? 0.f : m, vref = mv == -INFINITY ? 0.f : mv;
-          const float2 nref = make_float2(-ref, -ref);
-          float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            // 2^(m - M') s_v 2^kBoostLog (no more than 2^126: p is 0 there)
-            const float wm = fv[hf] * ex2_approx(fminf(ref + ev[hf] - vref, 112.f) + kBoostLog);
-            const float2 w2 = make_float2(wm, wm), f2 = make_float2(f[hf], f[hf]);
-#pragma unroll
-            for (int q4 = 0; q4 < 2; ++q4) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int k = 64 * hf + 32 * q4 + 2 * e;
-                float2 v = nref;
-                fma2(v, make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f2);
-                v.x = ex2_approx(v.x);
-                v.y = ex2_approx(v.y);
-                if (edge) {  // a NaN scale does not reach what is not seen
-                  if (s[k] == 0xff800000u) v.x = 0.f;
-                  if (s[k + 1] == 0xff800000u) v.y = 0.f;
-                }
-                sum = add2(sum, v);
-                float2 w = mul2(v, w2);
-                if (edge) {
-                  if (s[k] == 0xff800000u) w.x = 0.f;
-                  if (s[k + 1] == 0xff800000u) w.y = 0.f;
-                }
-                pk[e] = pack_h2(w.x, w.y);
+                for (int k = 0; k < 64; ++k)
+                  if (k > last) s[k] = 0xff800000u;
               }
-              tmem_st16(tS + 32 * hf + 16 * q4, pk);
+            };
+            auto half_max = [&](int hf) {
+              float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+              for (int k = 0; k < 64; k += 4) {
+                x0 = fmaxf(x0, fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
+                x1 = fmaxf(x1, fmaxf(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
+              }
+              x0 = fmaxf(x0, x1);
+              return x0 == -INFINITY ? x0 : x0 * (fcol * sc.sk[hf]);  // no factor is negative
+            };
+            tmem_wait_ld32<0>(s);
+            tmem_wait_ld32<32>(s);
+            mask(0);
+            mx[0] = half_max(0);
+            tmem_ld32<0>(tS + 64, s);
+            tmem_ld32<32>(tS + 96, s);
+            tmem_wait_ld32<0>(s);
+            tmem_wait_ld32<32>(s);
+            mask(1);
+            mx[1] = half_max(1);
+            const float mn = fmaxf(mx[0], mx[1]), vn = fmaxf(mx[0] + v_exp(0), mx[1] + v_exp(1));
+            if (mn > m + kLazy) {  // also from -inf
+              l *= ex2_approx(m - mn);
+              m = mn;
             }
-          }
-          l += sum.x + sum.y;
+            const bool grow = vn > mv + kLazy;
+            if (__any_sync(0xffffffffu, grow) && i > 0) {
+              const float cr = grow ? ex2_approx(mv - vn) : 1.f;
+#pragma unroll
+              for (int q4 = 0; q4 < 8; ++q4) {
+                uint32_t o[16];
+                tmem_ld16(tO + 16 * q4, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * cr);
+                tmem_st16(tO + 16 * q4, o);
+              }
+            }
+            if (grow) mv = vn;
+            const float ref = m == -INFINITY ? 0.f : m, vref = mv == -INFINITY ? 0.f : mv;
+            const float2 nref = make_float2(-ref, -ref);
+            float2 sum = make_float2(0.f, 0.f);
+            // weights of half hf, over S columns that are not needed any more
+            auto half_p = [&](int hf, uint32_t dst) {
+              // 2^(m - M') s_v 2^kBoostLog (no more than 2^126: p is 0 there)
+              const float wm = v_frac(hf) * ex2_approx(fminf(ref + v_exp(hf) - vref, 112.f) + kBoostLog);
+              const float f = fcol * sc.sk[hf];
+              const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f);
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4) {
+                uint32_t pk[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int k = 16 * q4 + 2 * e;
+                  float2 v = nref;
+                  fma2(v, make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f2);
+                  v.x = ex2_approx(v.x);
+                  v.y = ex2_approx(v.y);
+                  if constexpr (kEdge) {  // a NaN scale does not reach what is not seen
+                    if (s[k] == 0xff800000u) v.x = 0.f;
+                    if (s[k + 1] == 0xff800000u) v.y = 0.f;
+                  }
+                  sum = add2(sum, v);
+                  float2 w = mul2(v, w2);
+                  if constexpr (kEdge) {
+                    if (s[k] == 0xff800000u) w.x = 0.f;
+                    if (s[k + 1] == 0xff800000u) w.y = 0.f;
+                  }
+                  pk[e] = pack_h2(w.x, w.y);
+                }
+                tmem_st8(dst + 8 * q4, pk);
+              }
+            };
+            half_p(1, tS + 96);
+            tmem_ld32<0>(tS, s);
+            tmem_ld32<32>(tS + 32, s);
+            tmem_wait_ld32<0>(s);
+            tmem_wait_ld32<32>(s);
+            mask(0);
+            half_p(0, tS);
+            l += sum.x + sum.y;
+          };
+          if (edge) weigh(std::true_type()); else weigh(std::false_type());
           if (sc.minbad <= pos && valid) l = NAN;  // a value row that is not finite is seen
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&pfull[gr]);
         }
       }
-      // ---- the row's sums
+        done += steps;
+      }
+      // ---- the row's sums (its place is looked up again: no registers for
+      // it in the loop above)
+      const PrePart p = part_of(x);
+      const int rr = p.r0 + gr * 128 + row;
+      const bool valid = rr < snq[p.b] * a.G;
+      int* counters = static_cast<int*>(a.ws);
+      float4* records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.ws) +
+                                                  ((size_t)gridDim.x * 4 + 255) / 256 * 256);
       const bool whole = p.j0 == 0 && p.j1 == p.steps;
       const float4 st = make_float4(m, l, mv, 0.f);
       __nv_bfloat16* dst = a.o + p.b * a.os + (long long)(p.h * a.G + (valid ? rr % a.G : 0)) * a.oh +
@@ -534,12 +581,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           }
         }
       }
-      done += max(0, min(p.j1, max(p.ntile[0], p.ntile[1])) - p.j0);
       x = p.first + p.j1;
     }
   } else if (warp < 12) {
     // ================ converters
-    regs_dec<96>();
     const int ct = tid - 256;
     const int sub = ct >> 2, ch = ct & 3;  // 32 rows x 4 chunks a round
     uint4 kr[8], vr[8];
@@ -614,7 +659,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     bool live = true;
     for (long long x = lo; x < hi && live;) {
       const PrePart p = part_of(x);
-      const int L = slen[p.b], last = max(p.ntile[0], p.ntile[1]);
+      const int L = slen[p.b], last = max(p.nt0, p.nt1);
       const int j1 = min(p.j1, last);
       if (p.j0 < j1) {
         pages(p, p.j0, slab);
@@ -727,17 +772,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     }
   } else {
     // ================ products
-    regs_dec<32>();
+    regs_dec<80>();
     if (warp == 12) {
       const uint32_t q0 = smem_u32(sm + pl.q), k0 = smem_u32(sm + pl.k), v0 = smem_u32(sm + pl.v);
       uint32_t cnt = 0, nqf[2] = {0, 0}, np[2] = {0, 0}, nso[2] = {0, 0};
       bool live = true;
       for (long long x = lo; x < hi && live;) {
         const PrePart p = part_of(x);
-        const int j1 = min(p.j1, max(p.ntile[0], p.ntile[1]));
+        const int j1 = min(p.j1, max(p.nt0, p.nt1));
         // S of group gr, step j (its keys are in buffer `buf`)
         auto scores = [&](int gr, int buf) {
-          if (lane == 0) {
+          if (elect_one()) {
             tc_fence_after();
             const uint32_t d = tmem + gr * 128, qa = q0 + gr * kTileBytes, kb = k0 + buf * kTileBytes;
 #pragma unroll
@@ -750,52 +795,54 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           }
           __syncwarp();
         };
-        auto active = [&](int gr, int j) { return j < min(p.j1, p.ntile[gr]); };
+        auto active = [&](int gr, int j) { return j < min(p.j1, p.ntile(gr)); };
         if (p.j0 < j1) {
           const int buf = cnt & 1;
           if (!tc_wait_warp(&kfull[buf], (cnt >> 1) & 1, fail, lane)) { live = false; break; }
-          for (int gr = 0; gr < 2 && live; ++gr)
-            if (active(gr, p.j0)) {
+#pragma unroll
+          for (int gr = 0; gr < 2; ++gr)
+            if (live && active(gr, p.j0)) {
               live = tc_wait_warp(&qfull[gr], nqf[gr] & 1, fail, lane);
               ++nqf[gr];
               if (live) scores(gr, buf);
             }
           if (!live) break;
-          if (lane == 0) tc_commit(&kempty[buf]);
+          if (elect_one()) tc_commit(&kempty[buf]);
           __syncwarp();
         }
         for (int j = p.j0; j < j1 && live; ++j, ++cnt) {
           const int buf = cnt & 1, nbuf = buf ^ 1;
           if (!tc_wait_warp(&vfull[buf], (cnt >> 1) & 1, fail, lane)) { live = false; break; }
           bool more = false;
-          for (int gr = 0; gr < 2 && live; ++gr) {
-            if (!active(gr, j)) continue;
-            if (!tc_wait_warp(&pfull[gr], np[gr] & 1, fail, lane)) { live = false; break; }
+#pragma unroll
+          for (int gr = 0; gr < 2; ++gr) {
+            if (!live || !active(gr, j)) continue;
+            if (!tc_wait_warp(&pfull[gr], np[gr] & 1, fail, lane)) { live = false; continue; }
             ++np[gr];
             if (j == p.j0) {  // O's last sums have been read
-              if (nso[gr] > 0 && !tc_wait_warp(&oempty[gr], (nso[gr] - 1) & 1, fail, lane)) { live = false; break; }
+              if (nso[gr] > 0 && !tc_wait_warp(&oempty[gr], (nso[gr] - 1) & 1, fail, lane)) { live = false; continue; }
               ++nso[gr];
             }
-            if (lane == 0) {
+            if (elect_one()) {
               tc_fence_after();
               const uint32_t d = tmem + 256 + gr * 128, pa = tmem + gr * 128, vb = v0 + buf * kTileBytes;
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
-                mma_ts(d, pa + 8 * kk, sw128_desc(vb + (kk >> 2) * kHalf + (kk & 3) * 32), kIdesc,
+                mma_ts(d, pa + (kk < 4 ? 8 * kk : 64 + 8 * kk), sw128_desc(vb + (kk >> 2) * kHalf + (kk & 3) * 32), kIdesc,
                        j > p.j0 || kk > 0 ? 1u : 0u);
             }
             __syncwarp();
             if (active(gr, j + 1)) {
-              if (!more && !tc_wait_warp(&kfull[nbuf], ((cnt + 1) >> 1) & 1, fail, lane)) { live = false; break; }
+              if (!more && !tc_wait_warp(&kfull[nbuf], ((cnt + 1) >> 1) & 1, fail, lane)) { live = false; continue; }
               more = true;
               scores(gr, nbuf);
             } else {
-              if (lane == 0) tc_commit(&ofull[gr]);
+              if (elect_one()) tc_commit(&ofull[gr]);
               __syncwarp();
             }
           }
           if (!live) break;
-          if (lane == 0) {
+          if (elect_one()) {
             tc_commit(&vempty[buf]);
             if (more) tc_commit(&kempty[nbuf]);
           }
@@ -804,7 +851,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         x = p.first + p.j1;
       }
       // every product has ended before TMEM is freed
-      if (lane == 0 && works) {
+      if (works && elect_one()) {
         tc_commit(mdone);
         const uint64_t t0 = global_ns();
         while (!mbar_try_wait(mdone, 0) && global_ns() - t0 < kTcTimeoutNs) {
