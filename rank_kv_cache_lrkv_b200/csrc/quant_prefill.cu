@@ -26,8 +26,7 @@
 // The steps of all tiles are laid end to end and each CTA takes an equal
 // contiguous range (causal tiles differ in length, and a few tiles over a
 // long cache still fill the GPU).  A tile cut by a range's border goes
-// through records in the workspace, folded in order by the last CTA to
-// arrive.
+// through records in the workspace, which a second launch folds in order.
 #include <type_traits>
 
 #include "quant.cuh"
@@ -73,16 +72,38 @@ __host__ __device__ inline PrePlan pre_plan(int B) {
   return p;
 }
 
-// Records: [2 per CTA][33][256] float4: (m, l, M', -) of a row, then its 128
-// sums four at a time, rows side by side.
+// Workspace: the counters of the few-row kernel (not used here, and left
+// alone), a cut per CTA (sequence, head, row and last CTA of the tile that
+// begins in it and goes on elsewhere; last CTA -1: none), two records per CTA
+// as in quant_decode.cu, of [33][256] float4: (m, l, M', -) of a row, then its
+// 128 sums four at a time, rows side by side.
 constexpr size_t kPreRecord = (size_t)33 * kTileRows;
+__host__ __device__ inline size_t pre_cuts(int C) { return ((size_t)C * 4 + 255) / 256 * 256; }
+__host__ __device__ inline size_t pre_records(int C) {
+  return pre_cuts(C) + ((size_t)C * 16 + 255) / 256 * 256;
+}
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+// Shared-memory descriptors in halves: the upper one is the same for every
+// 128-byte-swizzled K-major tile, the lower one counts 16-byte units, so a
+// step within a tile is one addition (one thread issues all products).
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc,
                                        uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(alo), "r"(blo), "r"(kDescHi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t blo, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(blo), "r"(kDescHi), "r"(idesc), "r"(acc)
       : "memory");
 }
 // fp16 A and B, fp32 D, M = 128, N = 128, both K-major.
@@ -185,7 +206,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   int* snq = reinterpret_cast<int*>(sm + pl.nq);
   volatile int* fail = reinterpret_cast<volatile int*>(sm + pl.misc);
   uint32_t* taddr = reinterpret_cast<uint32_t*>(sm + pl.misc + 4);
-  volatile int* lastflag = fail + 2;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -305,6 +325,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + gr * 128, tO = tmem + lane_base + 256 + gr * 128;
     uint8_t* qs = sm + pl.q + gr * kTileBytes;
+    int4* cuts = reinterpret_cast<int4*>(static_cast<uint8_t*>(a.ws) + pre_cuts(gridDim.x));
+    if (tid == 0) cuts[blockIdx.x] = make_int4(0, 0, 0, -1);
     uint32_t ns = 0, no = 0;  // S tiles and O sums seen
     uint32_t done = 0;        // steps of the parts before
     for (long long x = lo; x < hi;) {
@@ -481,9 +503,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       const PrePart p = part_of(x);
       const int rr = p.r0 + gr * 128 + row;
       const bool valid = rr < snq[p.b] * a.G;
-      int* counters = static_cast<int*>(a.ws);
-      float4* records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.ws) +
-                                                  ((size_t)gridDim.x * 4 + 255) / 256 * 256);
+      float4* records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.ws) + pre_records(gridDim.x));
       const bool whole = p.j0 == 0 && p.j1 == p.steps;
       const float4 st = make_float4(m, l, mv, 0.f);
       __nv_bfloat16* dst = a.o + p.b * a.os + (long long)(p.h * a.G + (valid ? rr % a.G : 0)) * a.oh +
@@ -531,55 +551,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       }
       if (!whole) {
         rec[0] = st;
-        const int c0 = (int)(((p.first + 1) * C - 1) / total);
-        const int c1 = (int)(((p.first + p.steps) * C - 1) / total);
-        __threadfence();
-        named_bar(1, 256);
-        if (tid == 0) {
-          const int before = atomicAdd(&counters[c0], 1);
-          *lastflag = before == c1 - c0;
-          if (before == c1 - c0) counters[c0] = 0;
-        }
-        named_bar(1, 256);
-        const bool last = *lastflag != 0;
-        named_bar(1, 256);  // read before the next part writes it
-        if (last && valid) {
-          __threadfence();
-          auto part = [&](int cc) {
-            return records + ((size_t)2 * cc + (cc == c0 ? 1 : 0)) * kPreRecord + gr * 128 + row;
-          };
-          float M = -INFINITY, ls = 0.f, Z = -INFINITY;
-          for (int cc = c0; cc <= c1; ++cc) {
-            const float4 t = __ldcg(part(cc));
-            if (t.x == -INFINITY && t.y == 0.f) continue;
-            const float mn = fmaxf(M, t.x), mr = mn == -INFINITY ? 0.f : mn;
-            ls = ls * ex2_approx(M - mr) + t.y * ex2_approx(t.x - mr);
-            M = mn;
-            Z = fmaxf(Z, t.z);
-          }
-          const float zr = Z == -INFINITY ? 0.f : Z;
-          const float ff = ls == 0.f ? 0.f : ex2_approx(Z - M - kBoostLog) / ls;
-          for (int q8 = 0; q8 < 16; ++q8) {
-            float o[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = 0.f;
-            for (int cc = c0; cc <= c1; ++cc) {
-              const float4* t = part(cc);
-              const float4 stt = __ldcg(t);
-              if (stt.x == -INFINITY && stt.y == 0.f) continue;
-              const float fz = ex2_approx(stt.z - zr);
-              const float4 u = __ldcg(t + (size_t)(1 + 2 * q8) * kTileRows);
-              const float4 v = __ldcg(t + (size_t)(2 + 2 * q8) * kTileRows);
-              o[0] += u.x * fz; o[1] += u.y * fz; o[2] += u.z * fz; o[3] += u.w * fz;
-              o[4] += v.x * fz; o[5] += v.y * fz; o[6] += v.z * fz; o[7] += v.w * fz;
-            }
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack_bf16x2(ls == 0.f ? 0.f : o[2 * k] * ff, ls == 0.f ? 0.f : o[2 * k + 1] * ff);
-            *reinterpret_cast<uint4*>(dst + 8 * q8) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
+        // a tile that begins in this CTA and goes on in others: for the merge
+        if (tid == 0 && p.j0 == 0)
+          cuts[blockIdx.x] = make_int4(p.b, p.h, p.r0,
+                                       (int)(((p.first + p.steps) * C - 1) / total));
       }
       x = p.first + p.j1;
     }
@@ -774,80 +749,78 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     // ================ products
     regs_dec<80>();
     if (warp == 12) {
-      const uint32_t q0 = smem_u32(sm + pl.q), k0 = smem_u32(sm + pl.k), v0 = smem_u32(sm + pl.v);
-      uint32_t cnt = 0, nqf[2] = {0, 0}, np[2] = {0, 0}, nso[2] = {0, 0};
+      const uint32_t q0 = desc_lo(smem_u32(sm + pl.q)), k0 = desc_lo(smem_u32(sm + pl.k)),
+                     v0 = desc_lo(smem_u32(sm + pl.v));
+      uint32_t cnt = 0, np0 = 0, np1 = 0, ns0 = 0, ns1 = 0;  // steps; P tiles and sums per group
       bool live = true;
       for (long long x = lo; x < hi && live;) {
         const PrePart p = part_of(x);
         const int j1 = min(p.j1, max(p.nt0, p.nt1));
-        // S of group gr, step j (its keys are in buffer `buf`)
-        auto scores = [&](int gr, int buf) {
-          if (elect_one()) {
+        const int e0 = min(p.j1, p.nt0), e1 = min(p.j1, p.nt1);  // the groups' ends
+        bool ok = true;
+        if (p.j0 < j1 && elect_one()) {
+          // S of group gr, from key buffer `buf`; the issuer's own arrival
+          // hands on what it has seen of the converters (the scales)
+          auto scores = [&](int gr, uint32_t buf) {
             tc_fence_after();
-            const uint32_t d = tmem + gr * 128, qa = q0 + gr * kTileBytes, kb = k0 + buf * kTileBytes;
+            const uint32_t d = tmem + gr * 128, qa = q0 + gr * (kTileBytes >> 4),
+                           kb = k0 + buf * (kTileBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-              tc_mma(d, sw128_desc(qa + off), sw128_desc(kb + off), kIdesc, kk > 0 ? 1u : 0u);
+              const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+              mma_ss(d, qa + off, kb + off, kIdesc, kk > 0 ? 1u : 0u);
             }
             tc_commit(&sfull[gr]);
             mbar_arrive(&sfull[gr]);
+          };
+          auto sums = [&](int gr, uint32_t buf, bool first) {
+            tc_fence_after();
+            const uint32_t d = tmem + 256 + gr * 128, pa = tmem + gr * 128,
+                           vb = v0 + buf * (kTileBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts(d, pa + (kk < 4 ? 8 * kk : 64 + 8 * kk),
+                     vb + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), kIdesc,
+                     kk > 0 || !first ? 1u : 0u);
+          };
+          uint32_t cn = cnt, n0 = np0, n1 = np1;
+          ok = tc_wait(&kfull[cn & 1], (cn >> 1) & 1, fail);
+          if (ok && p.j0 < e0) {
+            ok = tc_wait(&qfull[0], ns0 & 1, fail);
+            if (ok) scores(0, cn & 1);
           }
-          __syncwarp();
-        };
-        auto active = [&](int gr, int j) { return j < min(p.j1, p.ntile(gr)); };
-        if (p.j0 < j1) {
-          const int buf = cnt & 1;
-          if (!tc_wait_warp(&kfull[buf], (cnt >> 1) & 1, fail, lane)) { live = false; break; }
-#pragma unroll
-          for (int gr = 0; gr < 2; ++gr)
-            if (live && active(gr, p.j0)) {
-              live = tc_wait_warp(&qfull[gr], nqf[gr] & 1, fail, lane);
-              ++nqf[gr];
-              if (live) scores(gr, buf);
-            }
-          if (!live) break;
-          if (elect_one()) tc_commit(&kempty[buf]);
-          __syncwarp();
-        }
-        for (int j = p.j0; j < j1 && live; ++j, ++cnt) {
-          const int buf = cnt & 1, nbuf = buf ^ 1;
-          if (!tc_wait_warp(&vfull[buf], (cnt >> 1) & 1, fail, lane)) { live = false; break; }
-          bool more = false;
-#pragma unroll
-          for (int gr = 0; gr < 2; ++gr) {
-            if (!live || !active(gr, j)) continue;
-            if (!tc_wait_warp(&pfull[gr], np[gr] & 1, fail, lane)) { live = false; continue; }
-            ++np[gr];
-            if (j == p.j0) {  // O's last sums have been read
-              if (nso[gr] > 0 && !tc_wait_warp(&oempty[gr], (nso[gr] - 1) & 1, fail, lane)) { live = false; continue; }
-              ++nso[gr];
-            }
-            if (elect_one()) {
-              tc_fence_after();
-              const uint32_t d = tmem + 256 + gr * 128, pa = tmem + gr * 128, vb = v0 + buf * kTileBytes;
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_ts(d, pa + (kk < 4 ? 8 * kk : 64 + 8 * kk), sw128_desc(vb + (kk >> 2) * kHalf + (kk & 3) * 32), kIdesc,
-                       j > p.j0 || kk > 0 ? 1u : 0u);
-            }
-            __syncwarp();
-            if (active(gr, j + 1)) {
-              if (!more && !tc_wait_warp(&kfull[nbuf], ((cnt + 1) >> 1) & 1, fail, lane)) { live = false; continue; }
-              more = true;
-              scores(gr, nbuf);
-            } else {
-              if (elect_one()) tc_commit(&ofull[gr]);
-              __syncwarp();
-            }
+          if (ok && p.j0 < e1) {
+            ok = tc_wait(&qfull[1], ns1 & 1, fail);
+            if (ok) scores(1, cn & 1);
           }
-          if (!live) break;
-          if (elect_one()) {
+          tc_commit(&kempty[cn & 1]);
+          for (int j = p.j0; j < j1 && ok; ++j, ++cn) {
+            const uint32_t buf = cn & 1;
+            ok = tc_wait(&vfull[buf], (cn >> 1) & 1, fail);
+            if (ok && j + 1 < j1) ok = tc_wait(&kfull[buf ^ 1], ((cn + 1) >> 1) & 1, fail);
+            if (ok && j < e0) {
+              ok = tc_wait(&pfull[0], n0++ & 1, fail);
+              // O's last sums have been read
+              if (ok && j == p.j0 && ns0 > 0) ok = tc_wait(&oempty[0], (ns0 - 1) & 1, fail);
+              if (!ok) break;
+              sums(0, buf, j == p.j0);
+              if (j + 1 < e0) scores(0, buf ^ 1); else tc_commit(&ofull[0]);
+            }
+            if (ok && j < e1) {
+              ok = tc_wait(&pfull[1], n1++ & 1, fail);
+              if (ok && j == p.j0 && ns1 > 0) ok = tc_wait(&oempty[1], (ns1 - 1) & 1, fail);
+              if (!ok) break;
+              sums(1, buf, j == p.j0);
+              if (j + 1 < e1) scores(1, buf ^ 1); else tc_commit(&ofull[1]);
+            }
             tc_commit(&vempty[buf]);
-            if (more) tc_commit(&kempty[nbuf]);
+            if (j + 1 < j1) tc_commit(&kempty[buf ^ 1]);
           }
-          __syncwarp();
         }
+        live = __all_sync(0xffffffffu, ok);
+        cnt += max(0, j1 - p.j0);
+        if (p.j0 < e0) { np0 += e0 - p.j0; ++ns0; }
+        if (p.j0 < e1) { np1 += e1 - p.j0; ++ns1; }
         x = p.first + p.j1;
       }
       // every product has ended before TMEM is freed
@@ -867,10 +840,48 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   if (tid == 0 && *fail) quant_error(c, kErrTimeout);
 }
 
+// The parts of the tiles that the ranges' borders cut, folded in order: one
+// CTA per (CTA in which the tile begins, 8 rows), a warp per row, 4 dims a
+// lane.  (Folded by the last CTA to arrive instead, one SM read all parts of
+// a tile: 127 us for 64 queries over 16K where the products take 25.)
+__global__ void __launch_bounds__(256) quant_merge_kernel(QuantAttnArgs a, int C) {
+  pdl_trigger();
+  pdl_wait();
+  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 cut = __ldcg(reinterpret_cast<const int4*>(static_cast<uint8_t*>(a.ws) + pre_cuts(C)) + c0);
+  if (cut.w < 0) return;
+  const int b = cut.x, h = cut.y, row = blockIdx.y * 8 + warp, rr = cut.z + row;
+  if (rr >= quant_queries(a, b) * a.G) return;
+  const float4* records = reinterpret_cast<const float4*>(static_cast<uint8_t*>(a.ws) + pre_records(C)) + row;
+  auto part = [&](int cc) { return records + ((size_t)2 * cc + (cc == c0 ? 1 : 0)) * kPreRecord; };
+  float M = -INFINITY, Z = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int cc = c0; cc <= cut.w; ++cc) {
+    const float4 t = __ldcg(part(cc)), s = __ldcg(part(cc) + (size_t)(1 + lane) * kTileRows);
+    if (t.x == -INFINITY && t.y == 0.f) continue;  // saw nothing (a NaN sum is something)
+    const float mn = fmaxf(M, t.x), mr = mn == -INFINITY ? 0.f : mn;
+    const float zn = fmaxf(Z, t.z), zr = zn == -INFINITY ? 0.f : zn;
+    l = l * ex2_approx(M - mr) + t.y * ex2_approx(t.x - mr);
+    const float f0 = ex2_approx(Z - zr), f1 = ex2_approx(t.z - zr);
+    M = mn;
+    Z = zn;
+    o.x = o.x * f0 + s.x * f1;
+    o.y = o.y * f0 + s.y * f1;
+    o.z = o.z * f0 + s.z * f1;
+    o.w = o.w * f0 + s.w * f1;
+  }
+  const float f = l == 0.f ? 0.f : ex2_approx(Z - M - kBoostLog) / l;
+  __nv_bfloat16* dst = a.o + b * a.os + (long long)(h * a.G + rr % a.G) * a.oh + (long long)(rr / a.G) * a.ot;
+  *reinterpret_cast<uint2*>(dst + 4 * lane) =
+      l == 0.f ? make_uint2(0, 0)
+               : make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+}
+
 }  // namespace
 
 size_t quant_prefill_workspace(int C) {
-  return ((size_t)C * 4 + 255) / 256 * 256 + (size_t)C * 2 * kPreRecord * 16;
+  return pre_records(C) + (size_t)C * 2 * kPreRecord * 16;
 }
 
 int quant_prefill_launch(const QuantAttnArgs& a, const DevInfo& info, cudaStream_t st) {
@@ -883,7 +894,12 @@ int quant_prefill_launch(const QuantAttnArgs& a, const DevInfo& info, cudaStream
   QuantAttnArgs args = a;
   int RT = (int)(((long long)a.n * a.G + kTileRows - 1) / kTileRows);
   void* p[] = {&args, &RT};
-  return launch_pdl(fn, dim3(info.sms), dim3(kPreThreads), smem, st, p) == cudaSuccess
+  if (launch_pdl(fn, dim3(info.sms), dim3(kPreThreads), smem, st, p) != cudaSuccess)
+    return LRKV_ERR_CUDA;
+  int C = info.sms;
+  void* pm[] = {&args, &C};
+  return launch_pdl((const void*)quant_merge_kernel, dim3(C, kTileRows / 8), dim3(256), 0, st, pm) ==
+                 cudaSuccess
              ? LRKV_OK
              : LRKV_ERR_CUDA;
 }
