@@ -5,19 +5,19 @@
 // fp16 times a power of two per row, the blocks' scales stay outside the
 // products.  Row r of a unit (sequence, KV head) is query r / G of q head
 // h G + r % G, so the heads of a group share their keys' tiles.  A tile is
-// 256 rows, two groups of 128 (the MMA's M); a step is 128 keys (two pages).
+// 256 rows, two groups of 128 (the MMA's M); a step is one page of 64 keys.
 //
 // Persistent, one CTA per SM, 16 warps:
 //  * warps 0-3 and 4-7: softmax of group 0 and 1, one row per thread (its
-//    TMEM lane).  S comes from TMEM, P goes back over S's columns as fp16,
-//    and the two groups take turns with the tensor cores: while one is in
-//    its softmax, the other's products run.
+//    TMEM lane).  S comes from TMEM, P goes back over S's columns as fp16.
+//    TMEM holds two S of 64 columns and one O per group, so a group's next
+//    scores are ready before its softmax ends.
 //  * warps 8-11: converters.  Codes from L2 into registers a step ahead, two
 //    bytes to two fp16 numbers, into the 128-byte-swizzled K-major tiles
 //    (keys as rows for Q K^T; the stored transpose of V is already K-major
 //    for P V).  The open block's bf16 rows become fp16 under a power of two.
-//  * warp 12, one lane: per step and group P V (A from TMEM) and then the
-//    next step's Q K^T.  A group's S barrier so tells that its O is at rest.
+//  * warp 12, one lane: per step and group P V (A from TMEM), then Q K^T of
+//    the step after the next into the S that P has just left.
 // A row keeps its references m (scores) and M' (scores + floor(log2 s_v)) as
 // long as they lag by at most 2^kLazy, so O is seldom rescaled; a weight is
 // then at most 2^(1 + kLazy + kBoostLog) = 2^15 and fp16's floor lies 2^-33
@@ -37,31 +37,35 @@ namespace lrkv {
 namespace {
 
 constexpr int kTileRows = 256;
-constexpr int kStepKeys = 128;
+constexpr int kStepKeys = kQBlock;
+constexpr int kRing = 4;                        // key and value tiles in flight
 constexpr int kPreThreads = 512;
-constexpr int kHalf = 128 * 128;                // bytes of 64 columns of 128 rows
-constexpr int kTileBytes = 2 * kHalf;           // a [128][128] fp16 tile
-constexpr int kScaleRing = 4;
+constexpr int kQHalf = 128 * 128;               // 64 dims of a group's 128 rows of q
+constexpr int kQGroup = 2 * kQHalf;
+constexpr int kKHalf = kStepKeys * 128;         // 64 dims of a step's keys
+constexpr int kTileBytes = 2 * kKHalf;          // a step's keys, or its values [128][64]
+// A step's scales are read until its P is written; the converters are at most
+// kRing + 2 steps ahead of that.
+constexpr int kScaleRing = 8;
 constexpr float kLazy = 6.f;
 constexpr float kBoostLog = 8.f;
 
 struct StepScales {
-  float sk[2], sv[2];
-  int ok[2];    // the page's tokens count
+  float sk, sv;
+  int ok;       // the page's tokens count
   int minbad;   // first open token whose value row is not finite
-  int pad;
 };
 
 struct PrePlan {
   int q, k, v, bars, scales, start, len, nq, sum, misc, total;
 };
-constexpr int kBars = 19;
+constexpr int kBars = 4 * kRing + 15;
 __host__ __device__ inline PrePlan pre_plan(int B) {
   PrePlan p;
   p.q = 0;
-  p.k = 2 * kTileBytes;
-  p.v = p.k + 2 * kTileBytes;
-  p.bars = p.v + 2 * kTileBytes;
+  p.k = 2 * kQGroup;
+  p.v = p.k + kRing * kTileBytes;
+  p.bars = p.v + kRing * kTileBytes;
   p.scales = (p.bars + kBars * 8 + 15) / 16 * 16;
   p.start = p.scales + kScaleRing * (int)sizeof(StepScales);
   p.sum = p.start + (B + 1) * 8;
@@ -106,8 +110,9 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t blo
       "r"(a_tmem), "r"(blo), "r"(kDescHi), "r"(idesc), "r"(acc)
       : "memory");
 }
-// fp16 A and B, fp32 D, M = 128, N = 128, both K-major.
-constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+// fp16 A and B, fp32 D, M = 128, both K-major; N = 64 keys or 128 dims.
+constexpr uint32_t kIdescS = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescO = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
@@ -196,9 +201,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   const QuantView& c = a.c;
   const PrePlan pl = pre_plan(c.B);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + pl.bars);
-  uint64_t *kfull = bars, *kempty = bars + 2, *vfull = bars + 4, *vempty = bars + 6,
-           *qfull = bars + 8, *sfull = bars + 10, *pfull = bars + 12, *ofull = bars + 14,
-           *oempty = bars + 16, *mdone = bars + 18;
+  // sfull, pfull: [group][S buffer]; odone: P V of the group's last step ended
+  uint64_t *kfull = bars, *kempty = kfull + kRing, *vfull = kempty + kRing, *vempty = vfull + kRing,
+           *qfull = vempty + kRing, *sfull = qfull + 2, *pfull = sfull + 4, *odone = pfull + 4,
+           *oempty = odone + 2, *mdone = oempty + 2;
   StepScales* scales = reinterpret_cast<StepScales*>(sm + pl.scales);
   long long* start = reinterpret_cast<long long*>(sm + pl.start);
   int* ssum = reinterpret_cast<int*>(sm + pl.sum);
@@ -210,15 +216,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
 
   if (tid == 0) {
     *fail = 0;
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(&kfull[i], 128);
       mbar_init(&kempty[i], 1);
       mbar_init(&vfull[i], 128);
       mbar_init(&vempty[i], 1);
-      mbar_init(&qfull[i], 128);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&sfull[i], 2);  // the products' commit and the issuer itself
       mbar_init(&pfull[i], 128);
-      mbar_init(&ofull[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&qfull[i], 128);
+      mbar_init(&odone[i], 1);
       mbar_init(&oempty[i], 128);
     }
     mbar_init(mdone, 1);
@@ -324,10 +334,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     const int gr = warp >> 2, row = tid & 127;  // TMEM lane = row of the group
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + gr * 128, tO = tmem + lane_base + 256 + gr * 128;
-    uint8_t* qs = sm + pl.q + gr * kTileBytes;
+    uint8_t* qs = sm + pl.q + gr * kQGroup;
     int4* cuts = reinterpret_cast<int4*>(static_cast<uint8_t*>(a.ws) + pre_cuts(gridDim.x));
     if (tid == 0) cuts[blockIdx.x] = make_int4(0, 0, 0, -1);
-    uint32_t ns = 0, no = 0;  // S tiles and O sums seen
+    uint32_t ns = 0;          // parity of the S tiles seen, a bit per buffer
+    uint32_t nd = 0;          // steps of this group in the parts before
     uint32_t done = 0;        // steps of the parts before
     for (long long x = lo; x < hi;) {
       float m = -INFINITY, l = 0.f, mv = -INFINITY;
@@ -341,7 +352,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         const int minpos = pos0 + (p.r0 + gr * 128) / a.G;
         n = min(p.j1, p.ntile(gr)) - p.j0;
         const uint32_t steps = max(0, min(p.j1, max(p.nt0, p.nt1)) - p.j0);
-      if (n > 0) {
+        if (n > 0) {
         // ---- the row of q: fp16, its largest element in [2^14, 2^15)
         float fcol;
         {
@@ -369,133 +380,106 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
                                        pack_h2(bf_lo(w[i].y) * up, bf_hi(w[i].y) * up),
                                        pack_h2(bf_lo(w[i].z) * up, bf_hi(w[i].z) * up),
                                        pack_h2(bf_lo(w[i].w) * up, bf_hi(w[i].w) * up));
-            *reinterpret_cast<uint4*>(qs + (i >> 3) * kHalf + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = h;
+            *reinterpret_cast<uint4*>(qs + (i >> 3) * kQHalf + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = h;
           }
         }
         fence_proxy_async_smem();
         mbar_arrive(&qfull[gr]);
         for (int i = 0; i < n; ++i) {
-          const int base = (p.j0 + i) * kStepKeys;
-          if (!tc_wait_warp(&sfull[gr], ns & 1, fail, lane)) break;
-          ++ns;
+          const int base = (p.j0 + i) * kStepKeys, sb = i & 1;
+          if (!tc_wait_warp(&sfull[2 * gr + sb], (ns >> sb) & 1, fail, lane)) break;
+          ns ^= 1u << sb;
           tc_fence_after();
-          // the second half of S stays in registers between the maximum and
-          // the weights, the first is read again (128 registers a thread)
+          const uint32_t tSb = tS + 64 * sb;
           uint32_t s[64];
-          tmem_ld32<0>(tS, s);
-          tmem_ld32<32>(tS + 32, s);
-          const StepScales& sc = scales[(done + i) % kScaleRing];
+          tmem_ld32<0>(tSb, s);
+          tmem_ld32<32>(tSb + 32, s);
+          const StepScales sc = scales[(done + i) % kScaleRing];
           // s_v = 2^ev fv, 1 <= fv < 2 (a NaN stays in fv)
-          auto v_exp = [&](int hf) {
-            const float sv = sc.sv[hf];
-            return sv != sv ? 0.f : (float)((int)(__float_as_uint(sv) >> 23) - 127);
-          };
-          auto v_frac = [&](int hf) {
-            const float sv = sc.sv[hf];
-            return sv != sv ? sv : __uint_as_float((__float_as_uint(sv) & 0x7fffffu) | 0x3f800000u);
-          };
-          float mx[2];
-          const bool edge = base + kStepKeys - 1 > minpos || !sc.ok[0] || !sc.ok[1];
+          const bool vnan = sc.sv != sc.sv;
+          const float ev = vnan ? 0.f : (float)((int)(__float_as_uint(sc.sv) >> 23) - 127);
+          const float fv = vnan ? sc.sv : __uint_as_float((__float_as_uint(sc.sv) & 0x7fffffu) | 0x3f800000u);
+          const float f = fcol * sc.sk;
+          tmem_wait_ld32<0>(s);
+          tmem_wait_ld32<32>(s);
+          const bool edge = base + kStepKeys - 1 > minpos || !sc.ok;
           // two bodies: masks cost every element two instructions and more
           auto weigh = [&](auto edge_c) {
             constexpr bool kEdge = decltype(edge_c)::value;
-            // what the row does not see of half hf
-            auto mask = [&](int hf) {
-              if constexpr (kEdge) {
-                const int last = sc.ok[hf] ? pos - base - 64 * hf : -1;
+            if constexpr (kEdge) {  // what the row does not see
+              const int last = sc.ok ? pos - base : -1;
 #pragma unroll
-                for (int k = 0; k < 64; ++k)
-                  if (k > last) s[k] = 0xff800000u;
-              }
-            };
-            auto half_max = [&](int hf) {
-              float x0 = -INFINITY, x1 = -INFINITY;
+              for (int k = 0; k < 64; ++k)
+                if (k > last) s[k] = 0xff800000u;
+            }
+            float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
-              for (int k = 0; k < 64; k += 4) {
-                x0 = fmaxf(x0, fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
-                x1 = fmaxf(x1, fmaxf(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
-              }
-              x0 = fmaxf(x0, x1);
-              return x0 == -INFINITY ? x0 : x0 * (fcol * sc.sk[hf]);  // no factor is negative
-            };
-            tmem_wait_ld32<0>(s);
-            tmem_wait_ld32<32>(s);
-            mask(0);
-            mx[0] = half_max(0);
-            tmem_ld32<0>(tS + 64, s);
-            tmem_ld32<32>(tS + 96, s);
-            tmem_wait_ld32<0>(s);
-            tmem_wait_ld32<32>(s);
-            mask(1);
-            mx[1] = half_max(1);
-            const float mn = fmaxf(mx[0], mx[1]), vn = fmaxf(mx[0] + v_exp(0), mx[1] + v_exp(1));
+            for (int k = 0; k < 64; k += 4) {
+              x0 = fmaxf(x0, fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
+              x1 = fmaxf(x1, fmaxf(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
+            }
+            x0 = fmaxf(x0, x1);
+            const float mn = x0 == -INFINITY ? x0 : x0 * f;  // f >= 0
+            const float vn = mn + ev;
             if (mn > m + kLazy) {  // also from -inf
               l *= ex2_approx(m - mn);
               m = mn;
             }
             const bool grow = vn > mv + kLazy;
             if (__any_sync(0xffffffffu, grow) && i > 0) {
-              const float cr = grow ? ex2_approx(mv - vn) : 1.f;
+              // the step before has been added; this one waits for P
+              if (tc_wait_warp(&odone[gr], (nd + i - 1) & 1, fail, lane)) {
+                tc_fence_after();
+                const float cr = grow ? ex2_approx(mv - vn) : 1.f;
 #pragma unroll
-              for (int q4 = 0; q4 < 8; ++q4) {
-                uint32_t o[16];
-                tmem_ld16(tO + 16 * q4, o);
+                for (int q4 = 0; q4 < 8; ++q4) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + 16 * q4, o);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * cr);
-                tmem_st16(tO + 16 * q4, o);
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * cr);
+                  tmem_st16(tO + 16 * q4, o);
+                }
               }
             }
             if (grow) mv = vn;
             const float ref = m == -INFINITY ? 0.f : m, vref = mv == -INFINITY ? 0.f : mv;
-            const float2 nref = make_float2(-ref, -ref);
+            // 2^(m - M') s_v 2^kBoostLog (no more than 2^126: p is 0 there)
+            const float wm = fv * ex2_approx(fminf(ref + ev - vref, 112.f) + kBoostLog);
+            const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f), nref = make_float2(-ref, -ref);
             float2 sum = make_float2(0.f, 0.f);
-            // weights of half hf, over S columns that are not needed any more
-            auto half_p = [&](int hf, uint32_t dst) {
-              // 2^(m - M') s_v 2^kBoostLog (no more than 2^126: p is 0 there)
-              const float wm = v_frac(hf) * ex2_approx(fminf(ref + v_exp(hf) - vref, 112.f) + kBoostLog);
-              const float f = fcol * sc.sk[hf];
-              const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f);
 #pragma unroll
-              for (int q4 = 0; q4 < 4; ++q4) {
-                uint32_t pk[8];
+            for (int q4 = 0; q4 < 4; ++q4) {
+              uint32_t pk[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int k = 16 * q4 + 2 * e;
-                  float2 v = nref;
-                  fma2(v, make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f2);
-                  v.x = ex2_approx(v.x);
-                  v.y = ex2_approx(v.y);
-                  if constexpr (kEdge) {  // a NaN scale does not reach what is not seen
-                    if (s[k] == 0xff800000u) v.x = 0.f;
-                    if (s[k + 1] == 0xff800000u) v.y = 0.f;
-                  }
-                  sum = add2(sum, v);
-                  float2 w = mul2(v, w2);
-                  if constexpr (kEdge) {
-                    if (s[k] == 0xff800000u) w.x = 0.f;
-                    if (s[k + 1] == 0xff800000u) w.y = 0.f;
-                  }
-                  pk[e] = pack_h2(w.x, w.y);
+              for (int e = 0; e < 8; ++e) {
+                const int k = 16 * q4 + 2 * e;
+                float2 v = nref;
+                fma2(v, make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f2);
+                v.x = ex2_approx(v.x);
+                v.y = ex2_approx(v.y);
+                if constexpr (kEdge) {  // a NaN scale does not reach what is not seen
+                  if (s[k] == 0xff800000u) v.x = 0.f;
+                  if (s[k + 1] == 0xff800000u) v.y = 0.f;
                 }
-                tmem_st8(dst + 8 * q4, pk);
+                sum = add2(sum, v);
+                float2 w = mul2(v, w2);
+                if constexpr (kEdge) {
+                  if (s[k] == 0xff800000u) w.x = 0.f;
+                  if (s[k + 1] == 0xff800000u) w.y = 0.f;
+                }
+                pk[e] = pack_h2(w.x, w.y);
               }
-            };
-            half_p(1, tS + 96);
-            tmem_ld32<0>(tS, s);
-            tmem_ld32<32>(tS + 32, s);
-            tmem_wait_ld32<0>(s);
-            tmem_wait_ld32<32>(s);
-            mask(0);
-            half_p(0, tS);
+              tmem_st8(tSb + 8 * q4, pk);
+            }
             l += sum.x + sum.y;
           };
           if (edge) weigh(std::true_type()); else weigh(std::false_type());
           if (sc.minbad <= pos && valid) l = NAN;  // a value row that is not finite is seen
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(&pfull[gr]);
+          mbar_arrive(&pfull[2 * gr + sb]);
         }
-      }
+        }
         done += steps;
       }
       // ---- the row's sums (its place is looked up again: no registers for
@@ -511,8 +495,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       float4* rec = records + ((size_t)2 * blockIdx.x + (p.j0 == 0 ? 1 : 0)) * kPreRecord + gr * 128 + row;
       const float fin = whole ? (l == 0.f ? 0.f : ex2_approx(mv - m - kBoostLog) / l) : 1.f;
       if (n > 0) {
-        tc_wait_warp(&ofull[gr], no & 1, fail, lane);
-        ++no;
+        tc_wait_warp(&odone[gr], (nd + n - 1) & 1, fail, lane);
+        nd += n;
         tc_fence_after();
       }
 #pragma unroll
@@ -562,40 +546,32 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     // ================ converters
     const int ct = tid - 256;
     const int sub = ct >> 2, ch = ct & 3;  // 32 rows x 4 chunks a round
-    uint4 kr[8], vr[8];
-    uint32_t cnt = 0;  // steps converted
-    const uint8_t* slab[2];
-    float2 nsc[2];  // their scales
-    // slabs of step j (nullptr: open, past the end or out of range)
-    auto pages = [&](const PrePart& p, int j, const uint8_t* (&s)[2]) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int pg = 2 * j + u;
-        s[u] = nullptr;
-        if ((pg + 1) * kQBlock <= slen[p.b]) {
-          s[u] = quant_slab(c, p.b, p.h, pg);
-          if (s[u]) nsc[u] = __ldg(reinterpret_cast<const float2*>(s[u] + 2 * kQSide));
-          else if (ct == 0) quant_error(c, kErrBadPage);
-        }
+    uint4 kr[4], vr[4];
+    uint32_t cnt = 0;     // steps converted
+    const uint8_t* slab;  // slab of a step (nullptr: open, or out of range)
+    float2 nsc;           // its scales
+    auto page = [&](const PrePart& p, int j) {
+      slab = nullptr;
+      if ((j + 1) * kQBlock <= slen[p.b]) {
+        slab = quant_slab(c, p.b, p.h, j);
+        if (slab) nsc = __ldg(reinterpret_cast<const float2*>(slab + 2 * kQSide));
+        else if (ct == 0) quant_error(c, kErrBadPage);
       }
     };
-    // keys: token 32 i + sub of the page, chunks ch and ch + 4 (i = 0, 1)
-    auto load_k = [&](const uint8_t* (&s)[2]) {
+    // keys: token 32 (i / 2) + sub, chunk ch + 4 (i % 2); a quarter warp then
+    // writes two rows' chunks of one half: no bank conflicts
+    auto load_k = [&]() {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          kr[4 * u + i] = s[u] ? __ldg(reinterpret_cast<const uint4*>(
-                                     s[u] + quant_k_chunk(32 * (i >> 1) + sub, ch + 4 * (i & 1))))
-                               : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i)
+        kr[i] = slab ? __ldg(reinterpret_cast<const uint4*>(
+                           slab + quant_k_chunk(32 * (i >> 1) + sub, ch + 4 * (i & 1))))
+                     : make_uint4(0, 0, 0, 0);
     };
-    auto load_v = [&](const uint8_t* (&s)[2]) {
+    auto load_v = [&]() {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          vr[4 * u + i] = s[u] ? __ldg(reinterpret_cast<const uint4*>(s[u] + kQSide + (32 * i + sub) * kQBlock + ch * 16))
-                               : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i)
+        vr[i] = slab ? __ldg(reinterpret_cast<const uint4*>(slab + kQSide + (32 * i + sub) * kQBlock + ch * 16))
+                     : make_uint4(0, 0, 0, 0);
     };
     // 16 codes -> 32 bytes of fp16 at chunks cc, cc + 1 of a swizzled row
     auto put = [&](uint8_t* rowp, int row, int cc, const uint4& w) {
@@ -637,90 +613,75 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       const int L = slen[p.b], last = max(p.nt0, p.nt1);
       const int j1 = min(p.j1, last);
       if (p.j0 < j1) {
-        pages(p, p.j0, slab);
-        load_k(slab);
+        page(p, p.j0);
+        load_k();
       }
       for (int j = p.j0; j < j1; ++j) {
-        const int buf = cnt & 1;
+        const int buf = cnt % kRing;
         uint8_t* kb = sm + pl.k + buf * kTileBytes;
         uint8_t* vb = sm + pl.v + buf * kTileBytes;
-        load_v(slab);
-        // the scales; the open block among the two pages, if any
-        int open = -1;
-        float sk[2] = {1.f, 1.f}, sv[2] = {1.f, 1.f};
-        int ok[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int pg = 2 * j + u;
-          ok[u] = slab[u] != nullptr;
-          if (slab[u]) {
-            sk[u] = nsc[u].x;
-            sv[u] = nsc[u].y;
-          } else if (pg * kQBlock < L && (pg + 1) * kQBlock > L) {
-            open = u;
-            ok[u] = 1;
-          }
+        load_v();
+        const bool open = !slab && (j + 1) * kQBlock > L;
+        float sk = 1.f, sv = 1.f;
+        if (slab) {
+          sk = nsc.x;
+          sv = nsc.y;
         }
-        if (cnt >= 2 && !tc_wait_warp(&kempty[buf], ((cnt >> 1) - 1) & 1, fail, lane)) { live = false; break; }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
+        const int ok = slab || open;
+        if (cnt >= kRing && !tc_wait_warp(&kempty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
+        if (!open) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int row = 64 * u + 32 * (i >> 1) + sub;
-            if (u != open)
-              put(kb + (i & 1) * kHalf + row * 128, row, 2 * ch, kr[4 * u + i]);
+            const int row = 32 * (i >> 1) + sub;
+            put(kb + (i & 1) * kKHalf + row * 128, row, 2 * ch, kr[i]);
           }
+        }
         int minbad = 0x7fffffff;
-        if (open >= 0) {
+        if (open) {
           // keys of the open block: thread = (token, half of the dims)
-          const int pg = 2 * j + open, tok = ct >> 1, side = ct & 1, row = 64 * open + tok;
-          const int nt = L - pg * kQBlock;
+          const int tok = ct >> 1, side = ct & 1;
+          const int nt = L - j * kQBlock;
           int bad;
-          int e = (int)(scan_open(quant_tail(c, p.b, p.h, 0, pg * kQBlock), nt, bad) >> 7) - 127;
+          int e = (int)(scan_open(quant_tail(c, p.b, p.h, 0, j * kQBlock), nt, bad) >> 7) - 127;
           e = max(e, -100);
           const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-          sk[open] = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
-          const uint4* src = reinterpret_cast<const uint4*>(quant_tail(c, p.b, p.h, 0, pg * kQBlock + tok)) + 8 * side;
+          sk = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+          const uint4* src = reinterpret_cast<const uint4*>(quant_tail(c, p.b, p.h, 0, j * kQBlock + tok)) + 8 * side;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint4 w = tok < nt ? src[i] : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(kb + side * kHalf + row * 128 + ((i ^ (row & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(kb + side * kKHalf + tok * 128 + ((i ^ (tok & 7)) << 4)) =
                 make_uint4(pack_h2(bf_lo(w.x) * up, bf_hi(w.x) * up),
                            pack_h2(bf_lo(w.y) * up, bf_hi(w.y) * up),
                            pack_h2(bf_lo(w.z) * up, bf_hi(w.z) * up),
                            pack_h2(bf_lo(w.w) * up, bf_hi(w.w) * up));
           }
-          const int ve = (int)(scan_open(quant_tail(c, p.b, p.h, 1, pg * kQBlock), nt, bad) >> 7) - 127;
-          if (bad < 64) minbad = pg * kQBlock + bad;
-          sv[open] = __uint_as_float((uint32_t)(127 - 7 + max(ve, -100)) << 23);
+          const int ve = (int)(scan_open(quant_tail(c, p.b, p.h, 1, j * kQBlock), nt, bad) >> 7) - 127;
+          if (bad < 64) minbad = j * kQBlock + bad;
+          sv = __uint_as_float((uint32_t)(127 - 7 + max(ve, -100)) << 23);
         }
         if (ct == 0) {
           StepScales* s = &scales[cnt % kScaleRing];
-          s->sk[0] = sk[0]; s->sk[1] = sk[1];
-          s->sv[0] = sv[0]; s->sv[1] = sv[1];
-          s->ok[0] = ok[0]; s->ok[1] = ok[1];
+          s->sk = sk;
+          s->sv = sv;
+          s->ok = ok;
           s->minbad = minbad;
         }
         fence_proxy_async_smem();
         mbar_arrive(&kfull[buf]);
         if (j + 1 < j1) {
-          pages(p, j + 1, slab);
-          load_k(slab);
+          page(p, j + 1);
+          load_k();
         }
-        if (cnt >= 2 && !tc_wait_warp(&vempty[buf], ((cnt >> 1) - 1) & 1, fail, lane)) { live = false; break; }
+        if (cnt >= kRing && !tc_wait_warp(&vempty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
+        if (!open) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = 32 * i + sub;
-            if (u != open) put(vb + u * kHalf + row * 128, row, 2 * ch, vr[4 * u + i]);
-          }
-        if (open >= 0) {
-          const int pg = 2 * j + open, row = ct;
-          const __nv_bfloat16* vt = quant_tail(c, p.b, p.h, 1, pg * kQBlock) + ct;
-          const int nt = L - pg * kQBlock;
-          const float down = sv[open];
-          const float up = __uint_as_float((254u << 23) - __float_as_uint(down));  // 1 / a power of two
+          for (int i = 0; i < 4; ++i) put(vb + (32 * i + sub) * 128, 32 * i + sub, 2 * ch, vr[i]);
+        } else {
+          // values of the open block: thread = dim
+          const __nv_bfloat16* vt = quant_tail(c, p.b, p.h, 1, j * kQBlock) + ct;
+          const int nt = L - j * kQBlock;
+          const float up = __uint_as_float((254u << 23) - __float_as_uint(sv));  // 1 / sv, a power of two
 #pragma unroll 1
           for (int cc = 0; cc < 8; ++cc) {
             uint32_t h[4];
@@ -735,7 +696,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
               }
               h[q] = pack_h2(v[0], v[1]);
             }
-            *reinterpret_cast<uint4*>(vb + open * kHalf + row * 128 + ((cc ^ (row & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(vb + ct * 128 + ((cc ^ (ct & 7)) << 4)) =
                 make_uint4(h[0], h[1], h[2], h[3]);
           }
         }
@@ -751,76 +712,82 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     if (warp == 12) {
       const uint32_t q0 = desc_lo(smem_u32(sm + pl.q)), k0 = desc_lo(smem_u32(sm + pl.k)),
                      v0 = desc_lo(smem_u32(sm + pl.v));
-      uint32_t cnt = 0, np0 = 0, np1 = 0, ns0 = 0, ns1 = 0;  // steps; P tiles and sums per group
+      // steps; per group the parity of its P tiles, a bit per buffer, and its
+      // parts
+      uint32_t cnt = 0, np0 = 0, np1 = 0, ns0 = 0, ns1 = 0;
       bool live = true;
       for (long long x = lo; x < hi && live;) {
         const PrePart p = part_of(x);
-        const int j1 = min(p.j1, max(p.nt0, p.nt1));
-        const int e0 = min(p.j1, p.nt0), e1 = min(p.j1, p.nt1);  // the groups' ends
+        const int j1 = min(p.j1, max(p.nt0, p.nt1)), n = max(0, j1 - p.j0);
+        // the groups' steps here
+        const int n0 = max(0, min(p.j1, p.nt0) - p.j0), n1 = max(0, min(p.j1, p.nt1) - p.j0);
         bool ok = true;
-        if (p.j0 < j1 && elect_one()) {
-          // S of group gr, from key buffer `buf`; the issuer's own arrival
-          // hands on what it has seen of the converters (the scales)
-          auto scores = [&](int gr, uint32_t buf) {
-            tc_fence_after();
-            const uint32_t d = tmem + gr * 128, qa = q0 + gr * (kTileBytes >> 4),
-                           kb = k0 + buf * (kTileBytes >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-              mma_ss(d, qa + off, kb + off, kIdesc, kk > 0 ? 1u : 0u);
-            }
-            tc_commit(&sfull[gr]);
-            mbar_arrive(&sfull[gr]);
-          };
-          auto sums = [&](int gr, uint32_t buf, bool first) {
-            tc_fence_after();
-            const uint32_t d = tmem + 256 + gr * 128, pa = tmem + gr * 128,
-                           vb = v0 + buf * (kTileBytes >> 4);
+        if (n > 0 && elect_one()) {
+          // S of group gr, step i; the issuer's own arrival hands on what it
+          // has seen of the converters (the scales)
+          auto scores = [&](int gr, int i) {
+            const uint32_t d = tmem + gr * 128 + (i & 1) * 64, qa = q0 + gr * (kQGroup >> 4),
+                           kb = k0 + ((cnt + i) % kRing) * (kTileBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_ts(d, pa + (kk < 4 ? 8 * kk : 64 + 8 * kk),
-                     vb + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), kIdesc,
-                     kk > 0 || !first ? 1u : 0u);
+              mma_ss(d, qa + (((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4),
+                     kb + (((kk >> 2) * kKHalf + (kk & 3) * 32) >> 4), kIdescS, kk > 0 ? 1u : 0u);
+            tc_commit(&sfull[2 * gr + (i & 1)]);
+            mbar_arrive(&sfull[2 * gr + (i & 1)]);
           };
-          uint32_t cn = cnt, n0 = np0, n1 = np1;
-          ok = tc_wait(&kfull[cn & 1], (cn >> 1) & 1, fail);
-          if (ok && p.j0 < e0) {
-            ok = tc_wait(&qfull[0], ns0 & 1, fail);
-            if (ok) scores(0, cn & 1);
+          auto sums = [&](int gr, int i) {
+            const uint32_t d = tmem + 256 + gr * 128, pa = tmem + gr * 128 + (i & 1) * 64,
+                           vb = v0 + ((cnt + i) % kRing) * (kTileBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts(d, pa + 8 * kk, vb + ((kk * 32) >> 4), kIdescO, kk > 0 || i > 0 ? 1u : 0u);
+            tc_commit(&odone[gr]);
+          };
+          auto keys = [&](int i) {
+            return tc_wait(&kfull[(cnt + i) % kRing], ((cnt + i) / kRing) & 1, fail);
+          };
+          // P of the group's step i
+          auto weights = [&](int gr, int i, uint32_t np) {
+            return tc_wait(&pfull[2 * gr + (i & 1)], ((np >> (i & 1)) ^ (i >> 1)) & 1, fail);
+          };
+          if (n0 > 0) ok = tc_wait(&qfull[0], ns0 & 1, fail);
+          if (ok && n1 > 0) ok = tc_wait(&qfull[1], ns1 & 1, fail);
+          for (int i = 0; i < 2 && i < n && ok; ++i) {
+            ok = keys(i);
+            if (!ok) break;
+            tc_fence_after();
+            if (i < n0) scores(0, i);
+            if (i < n1) scores(1, i);
+            tc_commit(&kempty[(cnt + i) % kRing]);
           }
-          if (ok && p.j0 < e1) {
-            ok = tc_wait(&qfull[1], ns1 & 1, fail);
-            if (ok) scores(1, cn & 1);
-          }
-          tc_commit(&kempty[cn & 1]);
-          for (int j = p.j0; j < j1 && ok; ++j, ++cn) {
-            const uint32_t buf = cn & 1;
-            ok = tc_wait(&vfull[buf], (cn >> 1) & 1, fail);
-            if (ok && j + 1 < j1) ok = tc_wait(&kfull[buf ^ 1], ((cn + 1) >> 1) & 1, fail);
-            if (ok && j < e0) {
-              ok = tc_wait(&pfull[0], n0++ & 1, fail);
+          for (int i = 0; i < n && ok; ++i) {
+            ok = tc_wait(&vfull[(cnt + i) % kRing], ((cnt + i) / kRing) & 1, fail);
+            if (ok && i + 2 < n) ok = keys(i + 2);
+            if (ok && i < n0) {
+              ok = weights(0, i, np0);
               // O's last sums have been read
-              if (ok && j == p.j0 && ns0 > 0) ok = tc_wait(&oempty[0], (ns0 - 1) & 1, fail);
+              if (ok && i == 0 && ns0 > 0) ok = tc_wait(&oempty[0], (ns0 - 1) & 1, fail);
               if (!ok) break;
-              sums(0, buf, j == p.j0);
-              if (j + 1 < e0) scores(0, buf ^ 1); else tc_commit(&ofull[0]);
+              tc_fence_after();
+              sums(0, i);
+              if (i + 2 < n0) scores(0, i + 2);
             }
-            if (ok && j < e1) {
-              ok = tc_wait(&pfull[1], n1++ & 1, fail);
-              if (ok && j == p.j0 && ns1 > 0) ok = tc_wait(&oempty[1], (ns1 - 1) & 1, fail);
+            if (ok && i < n1) {
+              ok = weights(1, i, np1);
+              if (ok && i == 0 && ns1 > 0) ok = tc_wait(&oempty[1], (ns1 - 1) & 1, fail);
               if (!ok) break;
-              sums(1, buf, j == p.j0);
-              if (j + 1 < e1) scores(1, buf ^ 1); else tc_commit(&ofull[1]);
+              tc_fence_after();
+              sums(1, i);
+              if (i + 2 < n1) scores(1, i + 2);
             }
-            tc_commit(&vempty[buf]);
-            if (j + 1 < j1) tc_commit(&kempty[buf ^ 1]);
+            tc_commit(&vempty[(cnt + i) % kRing]);
+            if (i + 2 < n) tc_commit(&kempty[(cnt + i + 2) % kRing]);
           }
         }
         live = __all_sync(0xffffffffu, ok);
-        cnt += max(0, j1 - p.j0);
-        if (p.j0 < e0) { np0 += e0 - p.j0; ++ns0; }
-        if (p.j0 < e1) { np1 += e1 - p.j0; ++ns1; }
+        cnt += n;
+        if (n0 > 0) { np0 ^= (((n0 + 1) >> 1) & 1) | (((n0 >> 1) & 1) << 1); ++ns0; }
+        if (n1 > 0) { np1 ^= (((n1 + 1) >> 1) & 1) | (((n1 >> 1) & 1) << 1); ++ns1; }
         x = p.first + p.j1;
       }
       // every product has ended before TMEM is freed
