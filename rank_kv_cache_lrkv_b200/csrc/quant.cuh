@@ -81,6 +81,32 @@ __device__ __forceinline__ void quant_half4(uint32_t w, uint32_t& lo, uint32_t& 
   }
 }
 
+// Bounded mbarrier wait of the attention kernels, which also gives up once the
+// CTA has failed.  Kept small: unrolled polls at some twenty places made a
+// kernel of 228 KB, and every role waited for its instructions.
+__device__ __forceinline__ bool quant_wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (i % 64 == 0) {
+      if (*fail) return false;
+      if (global_ns() - t0 > 2000000000ull) {
+        *fail = 1;
+        return false;
+      }
+    }
+  }
+}
+// The same, taken by lane 0 for the whole warp.
+__device__ __forceinline__ bool quant_wait_warp(uint64_t* bar, uint32_t parity, volatile int* fail,
+                                                int lane) {
+  int ok = 1;
+  if (lane == 0) ok = quant_wait(bar, parity, fail) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
 // Launch arguments of the append, read and attention kernels.
 struct QuantAppendArgs {
   QuantView c;

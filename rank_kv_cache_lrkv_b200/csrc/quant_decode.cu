@@ -315,7 +315,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
           const int i = (int)(xc - p.first);
           if ((i + 1) * kQBlock > L) break;
           const int s = n_read % D;
-          const bool ok = tc_wait_warp(&bar[s], (n_read / D) & 1, fail, lane);
+          const bool ok = quant_wait_warp(&bar[s], (n_read / D) & 1, fail, lane);
           const bool use = ok && !((bad >> s) & 1);
           ++n_read;
           if (use) {

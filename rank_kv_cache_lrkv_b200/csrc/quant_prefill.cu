@@ -57,7 +57,7 @@ struct StepScales {
 };
 
 struct PrePlan {
-  int q, k, v, bars, scales, start, len, nq, sum, misc, total;
+  int q, k, v, bars, scales, parts, start, len, nq, sum, misc, total;
 };
 constexpr int kBars = 4 * kRing + 15;
 __host__ __device__ inline PrePlan pre_plan(int B) {
@@ -67,7 +67,8 @@ __host__ __device__ inline PrePlan pre_plan(int B) {
   p.v = p.k + kRing * kTileBytes;
   p.bars = p.v + kRing * kTileBytes;
   p.scales = (p.bars + kBars * 8 + 15) / 16 * 16;
-  p.start = p.scales + kScaleRing * (int)sizeof(StepScales);
+  p.parts = p.scales + kScaleRing * (int)sizeof(StepScales);
+  p.start = p.parts + 8 * 48;
   p.sum = p.start + (B + 1) * 8;
   p.len = p.sum + B * 4;
   p.nq = p.len + B * 4;
@@ -185,13 +186,89 @@ __device__ __forceinline__ float2 add2(const float2 a, const float2 b) {
   return d;
 }
 
+// The line of steps, in shared memory: per sequence its start, the steps of
+// one KV head, its length and its queries.
+struct Line {
+  const long long* start;
+  const int *sum, *len, *nq;
+  int B, G;
+};
+// Steps that group gr of row tile rt of sequence b needs.
+__device__ __forceinline__ int group_steps(const Line& n, int b, int rt, int gr) {
+  const int R = n.nq[b] * n.G, r = rt * kTileRows + gr * 128;
+  if (r >= R) return 0;
+  const int maxpos = n.len[b] - n.nq[b] + min(R - 1, r + 127) / n.G;
+  return maxpos < 0 ? 0 : maxpos / kStepKeys + 1;
+}
+// Steps of a tile (its last group with rows needs most): one at least for
+// queries that see nothing (their zeros).
+__device__ __forceinline__ int tile_steps(const Line& n, int b, int rt) {
+  const int R = n.nq[b] * n.G, r = rt * kTileRows;
+  if (r >= R) return 0;
+  return max(1, group_steps(n, b, rt, r + 128 < R ? 1 : 0));
+}
+
 // A part of a tile: steps [j0, j1) of `steps` in this CTA's range, `first`
-// the line's index of its step 0; ntile(g): steps that group g needs.
+// the line's index of its step 0; nt0, nt1: steps that the groups need.
 struct PrePart {
   int b, h, r0, steps, j0, j1, nt0, nt1;
   long long first;
   __device__ __forceinline__ int ntile(int g) const { return g ? nt1 : nt0; }
 };
+
+// The part that step x of the line belongs to; a whole warp calls, its lanes
+// look at 32 heads or tiles at a time.
+__device__ __forceinline__ PrePart find_part(const Line n, long long x, long long hi) {
+  const int lane = threadIdx.x & 31;
+  PrePart p;
+  int l = 0, r = n.B;
+#pragma unroll 1
+  while (r - l > 1) {
+    const int mid = (l + r) >> 1;
+    if (n.start[mid] <= x) l = mid; else r = mid;
+  }
+  p.b = l;
+  long long in = x - n.start[l];
+  const int sum = n.sum[l];
+  p.h = 0;
+#pragma unroll 1
+  for (;; p.h += 32, in -= 32ll * sum) {
+    const uint32_t past = __ballot_sync(0xffffffffu, (lane + 1ll) * sum > in);
+    if (past) {
+      const int w = __ffs(past) - 1;
+      p.h += w;
+      in -= (long long)w * sum;
+      break;
+    }
+  }
+  int left = (int)in, rt = 0;
+#pragma unroll 1
+  for (;; rt += 32) {
+    const int s = tile_steps(n, l, rt + lane);
+    int incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, incl > left);
+    if (past) {
+      const int w = __ffs(past) - 1;
+      p.steps = __shfl_sync(0xffffffffu, s, w);
+      left -= __shfl_sync(0xffffffffu, incl, w) - p.steps;
+      rt += w;
+      break;
+    }
+    left -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  p.r0 = rt * kTileRows;
+  p.first = x - left;
+  p.j0 = left;  // x is the first of the range or the tile's first
+  p.j1 = (int)(min(hi, p.first + p.steps) - p.first);
+  p.nt0 = group_steps(n, l, rt, 0);
+  p.nt1 = group_steps(n, l, rt, 1);
+  return p;
+}
 
 template <bool kE4M3>
 __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttnArgs a, int RT) {
@@ -206,6 +283,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
            *qfull = vempty + kRing, *sfull = qfull + 2, *pfull = sfull + 4, *odone = pfull + 4,
            *oempty = odone + 2, *mdone = oempty + 2;
   StepScales* scales = reinterpret_cast<StepScales*>(sm + pl.scales);
+  PrePart* parts = reinterpret_cast<PrePart*>(sm + pl.parts);  // [8]
   long long* start = reinterpret_cast<long long*>(sm + pl.start);
   int* ssum = reinterpret_cast<int*>(sm + pl.sum);
   int* slen = reinterpret_cast<int*>(sm + pl.len);
@@ -239,33 +317,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   for (int b = tid; b < c.B; b += kPreThreads) {
     slen[b] = quant_len(c, b);
     snq[b] = quant_queries(a, b);
-    ssum[b] = 0;
   }
   if (warp == 12) {
     tmem_alloc(taddr, 512);
     tmem_relinquish();
   }
   __syncthreads();
-  // steps that group gr of row tile rt of sequence b needs
-  auto group_steps = [&](int b, int rt, int gr) {
-    const int R = snq[b] * a.G, lo_r = rt * kTileRows + gr * 128;
-    if (lo_r >= R) return 0;
-    const int maxpos = slen[b] - snq[b] + min(R - 1, lo_r + 127) / a.G;
-    return maxpos < 0 ? 0 : maxpos / kStepKeys + 1;
-  };
-  // steps of a tile: one at least for queries that see nothing (their zeros)
-  auto tile_steps = [&](int b, int rt) {
-    if (rt * kTileRows >= snq[b] * a.G) return 0;
-    return max(1, max(group_steps(b, rt, 0), group_steps(b, rt, 1)));
-  };
-  for (long long i = tid; i < (long long)c.B * RT; i += kPreThreads) {
-    const int b = (int)(i / RT), s = tile_steps(b, (int)(i - (long long)b * RT));
-    if (s) atomicAdd(&ssum[b], s);
+  const Line line = {start, ssum, slen, snq, c.B, a.G};
+  // a warp per sequence: the steps of its tiles
+#pragma unroll 1
+  for (int b = warp; b < c.B; b += kPreThreads / 32) {
+    int s = 0;
+#pragma unroll 1
+    for (int rt = lane; rt < RT; rt += 32) s += tile_steps(line, b, rt);
+    s = (int)__reduce_add_sync(0xffffffffu, (uint32_t)s);
+    if (lane == 0) ssum[b] = s;
   }
   __syncthreads();
   if (warp == 0) {
     const int per = (c.B + 31) / 32, b0 = min(c.B, lane * per), b1 = min(c.B, b0 + per);
     long long own = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) own += (long long)ssum[b] * c.H;
     long long incl = own;
 #pragma unroll
@@ -274,6 +346,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       if (lane >= o) incl += y;
     }
     long long e = incl - own;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       start[b] = e;
       e += (long long)ssum[b] * c.H;
@@ -290,43 +363,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   const long long lo = works ? total * blockIdx.x / C : 0;
   const long long hi = works ? total * (blockIdx.x + 1) / C : 0;
 
-  // the part that step x of the line belongs to (a whole warp calls)
-  auto part_of = [&](long long x) {
-    PrePart p;
-    int l = 0, r = c.B;
-    while (r - l > 1) {
-      const int mid = (l + r) >> 1;
-      if (start[mid] <= x) l = mid; else r = mid;
-    }
-    p.b = l;
-    const long long in = x - start[l];
-    p.h = (int)(in / ssum[l]);
-    int left = (int)(in - (long long)p.h * ssum[l]), rt = 0;
-    for (;; rt += 32) {
-      int s = tile_steps(l, rt + lane), incl = s;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, incl > left);
-      if (past) {
-        const int w = __ffs(past) - 1;
-        p.steps = __shfl_sync(0xffffffffu, s, w);
-        left -= __shfl_sync(0xffffffffu, incl, w) - p.steps;
-        rt += w;
-        break;
-      }
-      left -= __shfl_sync(0xffffffffu, incl, 31);
-    }
-    p.r0 = rt * kTileRows;
-    p.first = x - left;
-    p.j0 = left;  // x is the first of the range or the tile's first
-    p.j1 = (int)(min(hi, p.first + p.steps) - p.first);
-    p.nt0 = group_steps(l, rt, 0);
-    p.nt1 = group_steps(l, rt, 1);
-    return p;
-  };
+  auto part_of = [&](long long x) { return find_part(line, x, hi); };
 
   if (warp < 8) {
     // ================ softmax
@@ -345,6 +382,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       int n;  // this group's steps here
       {
         const PrePart p = part_of(x);
+        __syncwarp();
+        if (lane == 0) parts[warp] = p;  // for the end of the part
         const int nq = snq[p.b], pos0 = slen[p.b] - nq;
         const int rr = p.r0 + gr * 128 + row;
         const bool valid = rr < nq * a.G;
@@ -353,41 +392,49 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         n = min(p.j1, p.ntile(gr)) - p.j0;
         const uint32_t steps = max(0, min(p.j1, max(p.nt0, p.nt1)) - p.j0);
         if (n > 0) {
-        // ---- the row of q: fp16, its largest element in [2^14, 2^15)
-        float fcol;
+        // ---- the warp's 32 rows of q, one after the other (whole rows at a
+        // time): fp16, the largest element in [2^14, 2^15)
+        float fcol = 0.f;
         {
+          const int w0 = p.r0 + gr * 128 + (row & ~31), R = nq * a.G;
           const float sgn = a.scale < 0.f ? -1.f : 1.f;
-          uint4 w[16];
-          const __nv_bfloat16* src = a.q + p.b * a.qs + (long long)(p.h * a.G + (valid ? rr % a.G : 0)) * a.qh +
-                                     (long long)(valid ? rr / a.G : 0) * a.qt;
-          uint32_t mx = 0;
+          int tk = w0 / a.G, hd = w0 - tk * a.G;
+          const __nv_bfloat16* src = a.q + p.b * a.qs + (long long)(p.h * a.G) * a.qh + 4 * lane;
+#pragma unroll 1
+          for (int i0 = 0; i0 < 32; i0 += 8) {
+            uint2 w[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            w[i] = valid ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
-            mx = __vmaxu2(mx, w[i].x & 0x7fff7fffu);
-            mx = __vmaxu2(mx, w[i].y & 0x7fff7fffu);
-            mx = __vmaxu2(mx, w[i].z & 0x7fff7fffu);
-            mx = __vmaxu2(mx, w[i].w & 0x7fff7fffu);
-          }
-          mx = max(mx >> 16, mx & 0xffffu);
-          int e = (int)(mx >> 7) - 127;
-          e = mx == 0 || e == 128 ? 14 : max(e, -100);
-          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23) * sgn;
-          fcol = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * (fabsf(a.scale) * kLog2e);
+            for (int i = 0; i < 8; ++i) {
+              w[i] = w0 + i0 + i < R
+                         ? __ldg(reinterpret_cast<const uint2*>(src + (long long)hd * a.qh + (long long)tk * a.qt))
+                         : make_uint2(0, 0);
+              if (++hd == a.G) {
+                hd = 0;
+                ++tk;
+              }
+            }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint4 h = make_uint4(pack_h2(bf_lo(w[i].x) * up, bf_hi(w[i].x) * up),
-                                       pack_h2(bf_lo(w[i].y) * up, bf_hi(w[i].y) * up),
-                                       pack_h2(bf_lo(w[i].z) * up, bf_hi(w[i].z) * up),
-                                       pack_h2(bf_lo(w[i].w) * up, bf_hi(w[i].w) * up));
-            *reinterpret_cast<uint4*>(qs + (i >> 3) * kQHalf + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = h;
+            for (int i = 0; i < 8; ++i) {
+              uint32_t mx = __vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu);
+              mx = __reduce_max_sync(0xffffffffu, max(mx >> 16, mx & 0xffffu));
+              int e = (int)(mx >> 7) - 127;
+              e = mx == 0 || e == 128 ? 14 : max(e, -100);
+              const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23) * sgn;
+              if (lane == i0 + i)
+                fcol = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * (fabsf(a.scale) * kLog2e);
+              const int rw = (row & ~31) + i0 + i;
+              *reinterpret_cast<uint2*>(qs + (lane >> 4) * kQHalf + rw * 128 +
+                                        ((((lane & 15) >> 1) ^ (rw & 7)) << 4) + (lane & 1) * 8) =
+                  make_uint2(pack_h2(bf_lo(w[i].x) * up, bf_hi(w[i].x) * up),
+                             pack_h2(bf_lo(w[i].y) * up, bf_hi(w[i].y) * up));
+            }
           }
         }
         fence_proxy_async_smem();
         mbar_arrive(&qfull[gr]);
         for (int i = 0; i < n; ++i) {
           const int base = (p.j0 + i) * kStepKeys, sb = i & 1;
-          if (!tc_wait_warp(&sfull[2 * gr + sb], (ns >> sb) & 1, fail, lane)) break;
+          if (!quant_wait_warp(&sfull[2 * gr + sb], (ns >> sb) & 1, fail, lane)) break;
           ns ^= 1u << sb;
           tc_fence_after();
           const uint32_t tSb = tS + 64 * sb;
@@ -403,50 +450,53 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           tmem_wait_ld32<0>(s);
           tmem_wait_ld32<32>(s);
           const bool edge = base + kStepKeys - 1 > minpos || !sc.ok;
-          // two bodies: masks cost every element two instructions and more
-          auto weigh = [&](auto edge_c) {
-            constexpr bool kEdge = decltype(edge_c)::value;
-            if constexpr (kEdge) {  // what the row does not see
-              const int last = sc.ok ? pos - base : -1;
+          // twice: masks cost every element two instructions and more
+          float x0 = -INFINITY, x1 = -INFINITY;
+          if (edge) {
+            const int last = sc.ok ? pos - base : -1;
 #pragma unroll
-              for (int k = 0; k < 64; ++k)
-                if (k > last) s[k] = 0xff800000u;
+            for (int k = 0; k < 64; ++k) {
+              if (k > last) s[k] = 0xff800000u;
+              x0 = fmaxf(x0, __uint_as_float(s[k]));
             }
-            float x0 = -INFINITY, x1 = -INFINITY;
+          } else {
 #pragma unroll
             for (int k = 0; k < 64; k += 4) {
               x0 = fmaxf(x0, fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
               x1 = fmaxf(x1, fmaxf(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
             }
             x0 = fmaxf(x0, x1);
-            const float mn = x0 == -INFINITY ? x0 : x0 * f;  // f >= 0
-            const float vn = mn + ev;
-            if (mn > m + kLazy) {  // also from -inf
-              l *= ex2_approx(m - mn);
-              m = mn;
-            }
-            const bool grow = vn > mv + kLazy;
-            if (__any_sync(0xffffffffu, grow) && i > 0) {
-              // the step before has been added; this one waits for P
-              if (tc_wait_warp(&odone[gr], (nd + i - 1) & 1, fail, lane)) {
-                tc_fence_after();
-                const float cr = grow ? ex2_approx(mv - vn) : 1.f;
+          }
+          const float mn = x0 == -INFINITY ? x0 : x0 * f;  // f >= 0
+          const float vn = mn + ev;
+          if (mn > m + kLazy) {  // also from -inf
+            l *= ex2_approx(m - mn);
+            m = mn;
+          }
+          const bool grow = vn > mv + kLazy;
+          if (__any_sync(0xffffffffu, grow) && i > 0) {
+            // the step before has been added; this one waits for P
+            if (quant_wait_warp(&odone[gr], (nd + i - 1) & 1, fail, lane)) {
+              tc_fence_after();
+              const float cr = grow ? ex2_approx(mv - vn) : 1.f;
+#pragma unroll 1
+              for (int q4 = 0; q4 < 8; ++q4) {
+                uint32_t o[16];
+                tmem_ld16(tO + 16 * q4, o);
 #pragma unroll
-                for (int q4 = 0; q4 < 8; ++q4) {
-                  uint32_t o[16];
-                  tmem_ld16(tO + 16 * q4, o);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * cr);
-                  tmem_st16(tO + 16 * q4, o);
-                }
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * cr);
+                tmem_st16(tO + 16 * q4, o);
               }
             }
-            if (grow) mv = vn;
-            const float ref = m == -INFINITY ? 0.f : m, vref = mv == -INFINITY ? 0.f : mv;
-            // 2^(m - M') s_v 2^kBoostLog (no more than 2^126: p is 0 there)
-            const float wm = fv * ex2_approx(fminf(ref + ev - vref, 112.f) + kBoostLog);
-            const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f), nref = make_float2(-ref, -ref);
-            float2 sum = make_float2(0.f, 0.f);
+          }
+          if (grow) mv = vn;
+          const float ref = m == -INFINITY ? 0.f : m, vref = mv == -INFINITY ? 0.f : mv;
+          // 2^(m - M') s_v 2^kBoostLog (no more than 2^126: p is 0 there)
+          const float wm = fv * ex2_approx(fminf(ref + ev - vref, 112.f) + kBoostLog);
+          const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f), nref = make_float2(-ref, -ref);
+          float2 sum = make_float2(0.f, 0.f);
+          auto weigh = [&](auto edge_c) {
+            constexpr bool kEdge = decltype(edge_c)::value;
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) {
               uint32_t pk[8];
@@ -457,23 +507,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
                 fma2(v, make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f2);
                 v.x = ex2_approx(v.x);
                 v.y = ex2_approx(v.y);
+                float2 w = mul2(v, w2);
                 if constexpr (kEdge) {  // a NaN scale does not reach what is not seen
-                  if (s[k] == 0xff800000u) v.x = 0.f;
-                  if (s[k + 1] == 0xff800000u) v.y = 0.f;
+                  if (s[k] == 0xff800000u) v.x = w.x = 0.f;
+                  if (s[k + 1] == 0xff800000u) v.y = w.y = 0.f;
                 }
                 sum = add2(sum, v);
-                float2 w = mul2(v, w2);
-                if constexpr (kEdge) {
-                  if (s[k] == 0xff800000u) w.x = 0.f;
-                  if (s[k + 1] == 0xff800000u) w.y = 0.f;
-                }
                 pk[e] = pack_h2(w.x, w.y);
               }
               tmem_st8(tSb + 8 * q4, pk);
             }
-            l += sum.x + sum.y;
           };
           if (edge) weigh(std::true_type()); else weigh(std::false_type());
+          l += sum.x + sum.y;
           if (sc.minbad <= pos && valid) l = NAN;  // a value row that is not finite is seen
           tmem_wait_st();
           tc_fence_before();
@@ -482,24 +528,21 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         }
         done += steps;
       }
-      // ---- the row's sums (its place is looked up again: no registers for
-      // it in the loop above)
-      const PrePart p = part_of(x);
-      const int rr = p.r0 + gr * 128 + row;
-      const bool valid = rr < snq[p.b] * a.G;
+      // ---- the row's sums (no registers for its place in the loop above)
+      __syncwarp();
+      const PrePart p = parts[warp];
       float4* records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.ws) + pre_records(gridDim.x));
       const bool whole = p.j0 == 0 && p.j1 == p.steps;
       const float4 st = make_float4(m, l, mv, 0.f);
-      __nv_bfloat16* dst = a.o + p.b * a.os + (long long)(p.h * a.G + (valid ? rr % a.G : 0)) * a.oh +
-                           (long long)(valid ? rr / a.G : 0) * a.ot;
       float4* rec = records + ((size_t)2 * blockIdx.x + (p.j0 == 0 ? 1 : 0)) * kPreRecord + gr * 128 + row;
-      const float fin = whole ? (l == 0.f ? 0.f : ex2_approx(mv - m - kBoostLog) / l) : 1.f;
+      const float fin = l == 0.f ? 0.f : ex2_approx(mv - m - kBoostLog) / l;
       if (n > 0) {
-        tc_wait_warp(&odone[gr], (nd + n - 1) & 1, fail, lane);
+        quant_wait_warp(&odone[gr], (nd + n - 1) & 1, fail, lane);
         nd += n;
         tc_fence_after();
       }
-#pragma unroll
+      // (unrolled once: O's registers are the loop's)
+#pragma unroll 1
       for (int q4 = 0; q4 < 4; ++q4) {
         uint32_t o[32];
         if (n > 0) {
@@ -510,16 +553,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
         if (whole) {
-          if (valid) {
+          // rows as bf16 where q's were (its products have ended), chunks of
+          // 16 bytes turned by the row
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = pack_bf16x2(l == 0.f ? 0.f : __uint_as_float(o[8 * e + 2 * k]) * fin,
-                                   l == 0.f ? 0.f : __uint_as_float(o[8 * e + 2 * k + 1]) * fin);
-              *reinterpret_cast<uint4*>(dst + 32 * q4 + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int k = 0; k < 4; ++k)
+              w[k] = l == 0.f ? 0u
+                              : pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * fin,
+                                            __uint_as_float(o[8 * e + 2 * k + 1]) * fin);
+            *reinterpret_cast<uint4*>(qs + row * 256 + (((4 * q4 + e) ^ (row & 15)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
 #pragma unroll
@@ -527,6 +572,23 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
             rec[(size_t)(1 + 8 * q4 + e) * kTileRows] =
                 make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                             __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+        }
+      }
+      if (whole) {
+        __syncwarp();
+        // two whole rows of the warp's 32 at a time
+        const int w0 = row & ~31, R = snq[p.b] * a.G, ch = lane & 15;
+        int r = p.r0 + gr * 128 + w0 + (lane >> 4);
+        int tk = r / a.G, hd = r - tk * a.G;
+        __nv_bfloat16* dst = a.o + p.b * a.os + (long long)(p.h * a.G) * a.oh + 8 * ch;
+#pragma unroll 4
+        for (int i = 0; i < 32; i += 2) {
+          const int rw = w0 + i + (lane >> 4);
+          if (r < R)
+            *reinterpret_cast<uint4*>(dst + (long long)hd * a.oh + (long long)tk * a.ot) =
+                *reinterpret_cast<const uint4*>(qs + rw * 256 + ((ch ^ (rw & 15)) << 4));
+          r += 2;
+          for (hd += 2; hd >= a.G; hd -= a.G) ++tk;
         }
       }
       if (n > 0) {
@@ -628,7 +690,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           sv = nsc.y;
         }
         const int ok = slab || open;
-        if (cnt >= kRing && !tc_wait_warp(&kempty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
+        if (cnt >= kRing && !quant_wait_warp(&kempty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
         if (!open) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -673,7 +735,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           page(p, j + 1);
           load_k();
         }
-        if (cnt >= kRing && !tc_wait_warp(&vempty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
+        if (cnt >= kRing && !quant_wait_warp(&vempty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
         if (!open) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) put(vb + (32 * i + sub) * 128, 32 * i + sub, 2 * ch, vr[i]);
@@ -744,14 +806,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
             tc_commit(&odone[gr]);
           };
           auto keys = [&](int i) {
-            return tc_wait(&kfull[(cnt + i) % kRing], ((cnt + i) / kRing) & 1, fail);
+            return quant_wait(&kfull[(cnt + i) % kRing], ((cnt + i) / kRing) & 1, fail);
           };
           // P of the group's step i
           auto weights = [&](int gr, int i, uint32_t np) {
-            return tc_wait(&pfull[2 * gr + (i & 1)], ((np >> (i & 1)) ^ (i >> 1)) & 1, fail);
+            return quant_wait(&pfull[2 * gr + (i & 1)], ((np >> (i & 1)) ^ (i >> 1)) & 1, fail);
           };
-          if (n0 > 0) ok = tc_wait(&qfull[0], ns0 & 1, fail);
-          if (ok && n1 > 0) ok = tc_wait(&qfull[1], ns1 & 1, fail);
+          if (n0 > 0) ok = quant_wait(&qfull[0], ns0 & 1, fail);
+          if (ok && n1 > 0) ok = quant_wait(&qfull[1], ns1 & 1, fail);
           for (int i = 0; i < 2 && i < n && ok; ++i) {
             ok = keys(i);
             if (!ok) break;
@@ -761,12 +823,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
             tc_commit(&kempty[(cnt + i) % kRing]);
           }
           for (int i = 0; i < n && ok; ++i) {
-            ok = tc_wait(&vfull[(cnt + i) % kRing], ((cnt + i) / kRing) & 1, fail);
+            ok = quant_wait(&vfull[(cnt + i) % kRing], ((cnt + i) / kRing) & 1, fail);
             if (ok && i + 2 < n) ok = keys(i + 2);
             if (ok && i < n0) {
               ok = weights(0, i, np0);
               // O's last sums have been read
-              if (ok && i == 0 && ns0 > 0) ok = tc_wait(&oempty[0], (ns0 - 1) & 1, fail);
+              if (ok && i == 0 && ns0 > 0) ok = quant_wait(&oempty[0], (ns0 - 1) & 1, fail);
               if (!ok) break;
               tc_fence_after();
               sums(0, i);
@@ -774,7 +836,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
             }
             if (ok && i < n1) {
               ok = weights(1, i, np1);
-              if (ok && i == 0 && ns1 > 0) ok = tc_wait(&oempty[1], (ns1 - 1) & 1, fail);
+              if (ok && i == 0 && ns1 > 0) ok = quant_wait(&oempty[1], (ns1 - 1) & 1, fail);
               if (!ok) break;
               tc_fence_after();
               sums(1, i);
