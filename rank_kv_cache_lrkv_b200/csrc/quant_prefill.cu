@@ -47,6 +47,9 @@ constexpr int kTileBytes = 2 * kKHalf;          // a step's keys, or its values 
 // A step's scales are read until its P is written; the converters are at most
 // kRing + 2 steps ahead of that.
 constexpr int kScaleRing = 8;
+// A tile's start and end (its rows of q and o, the empty pipeline) take about
+// as long as this many steps; the ranges count them.
+constexpr int kTileSteps = 4;
 constexpr float kLazy = 6.f;
 constexpr float kBoostLog = 8.f;
 
@@ -186,8 +189,8 @@ __device__ __forceinline__ float2 add2(const float2 a, const float2 b) {
   return d;
 }
 
-// The line of steps, in shared memory: per sequence its start, the steps of
-// one KV head, its length and its queries.
+// The line, in shared memory: per sequence its start, what one KV head takes
+// of it, its length and its queries.
 struct Line {
   const long long* start;
   const int *sum, *len, *nq;
@@ -207,18 +210,33 @@ __device__ __forceinline__ int tile_steps(const Line& n, int b, int rt) {
   if (r >= R) return 0;
   return max(1, group_steps(n, b, rt, r + 128 < R ? 1 : 0));
 }
+// What a tile takes of the line.
+__device__ __forceinline__ int tile_length(const Line& n, int b, int rt) {
+  const int s = tile_steps(n, b, rt);
+  return s ? s + kTileSteps : 0;
+}
 
-// A part of a tile: steps [j0, j1) of `steps` in this CTA's range, `first`
-// the line's index of its step 0; nt0, nt1: steps that the groups need.
+// A part of a tile: steps [j0, j1) of `steps` in this CTA's range (j1 <= j0:
+// none), `first` the line's index of its step 0; nt0, nt1: steps that the
+// groups need.
 struct PrePart {
   int b, h, r0, steps, j0, j1, nt0, nt1;
   long long first;
   __device__ __forceinline__ int ntile(int g) const { return g ? nt1 : nt0; }
 };
 
-// The part that step x of the line belongs to; a whole warp calls, its lanes
+// The rest of a part whose place (b, h, r0) and first are known.
+__device__ __forceinline__ void fill_part(const Line& n, PrePart& p, long long x, long long hi) {
+  const int rt = p.r0 / kTileRows;
+  p.nt0 = group_steps(n, p.b, rt, 0);
+  p.nt1 = group_steps(n, p.b, rt, 1);
+  p.steps = max(1, max(p.nt0, p.nt1));
+  p.j0 = (int)max(0ll, x - p.first);
+  p.j1 = (int)(min(hi, p.first + p.steps) - p.first);
+}
+// The part that place x of the line belongs to; a whole warp calls, its lanes
 // look at 32 heads or tiles at a time.
-__device__ __forceinline__ PrePart find_part(const Line n, long long x, long long hi) {
+__device__ __forceinline__ PrePart find_part(const Line& n, long long x, long long hi) {
   const int lane = threadIdx.x & 31;
   PrePart p;
   int l = 0, r = n.B;
@@ -244,7 +262,7 @@ __device__ __forceinline__ PrePart find_part(const Line n, long long x, long lon
   int left = (int)in, rt = 0;
 #pragma unroll 1
   for (;; rt += 32) {
-    const int s = tile_steps(n, l, rt + lane);
+    const int s = tile_length(n, l, rt + lane);
     int incl = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -254,20 +272,32 @@ __device__ __forceinline__ PrePart find_part(const Line n, long long x, long lon
     const uint32_t past = __ballot_sync(0xffffffffu, incl > left);
     if (past) {
       const int w = __ffs(past) - 1;
-      p.steps = __shfl_sync(0xffffffffu, s, w);
-      left -= __shfl_sync(0xffffffffu, incl, w) - p.steps;
+      left -= __shfl_sync(0xffffffffu, incl - s, w);
       rt += w;
       break;
     }
     left -= __shfl_sync(0xffffffffu, incl, 31);
   }
   p.r0 = rt * kTileRows;
-  p.first = x - left;
-  p.j0 = left;  // x is the first of the range or the tile's first
-  p.j1 = (int)(min(hi, p.first + p.steps) - p.first);
-  p.nt0 = group_steps(n, l, rt, 0);
-  p.nt1 = group_steps(n, l, rt, 1);
+  p.first = x - left + kTileSteps;
+  fill_part(n, p, x, hi);
   return p;
+}
+// The part after p, at the place x where p's tile ends on the line.
+__device__ __forceinline__ PrePart next_part(const Line& n, const PrePart& p, long long x,
+                                             long long hi, int H) {
+  PrePart q = p;
+  q.r0 += kTileRows;
+  if (q.r0 >= n.nq[q.b] * n.G) {
+    q.r0 = 0;
+    if (++q.h == H) {
+      q.h = 0;
+      do ++q.b; while (n.sum[q.b] == 0);
+    }
+  }
+  q.first = x + kTileSteps;
+  fill_part(n, q, x, hi);
+  return q;
 }
 
 template <bool kE4M3>
@@ -329,7 +359,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   for (int b = warp; b < c.B; b += kPreThreads / 32) {
     int s = 0;
 #pragma unroll 1
-    for (int rt = lane; rt < RT; rt += 32) s += tile_steps(line, b, rt);
+    for (int rt = lane; rt < RT; rt += 32) s += tile_length(line, b, rt);
     s = (int)__reduce_add_sync(0xffffffffu, (uint32_t)s);
     if (lane == 0) ssum[b] = s;
   }
@@ -363,7 +393,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   const long long lo = works ? total * blockIdx.x / C : 0;
   const long long hi = works ? total * (blockIdx.x + 1) / C : 0;
 
-  auto part_of = [&](long long x) { return find_part(line, x, hi); };
+  // the parts of this range, one after the other: `x` is where the part begins
+  auto advance = [&](PrePart& p, long long& x) {
+    x = p.first + max(p.j1, 0);
+    if (x < hi) p = next_part(line, p, x, hi, c.H);
+  };
 
   if (warp < 8) {
     // ================ softmax
@@ -377,13 +411,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     uint32_t ns = 0;          // parity of the S tiles seen, a bit per buffer
     uint32_t nd = 0;          // steps of this group in the parts before
     uint32_t done = 0;        // steps of the parts before
+    // the part lives in shared memory: no registers for it in the loops below
+    if (lo < hi) {
+      const PrePart p = find_part(line, lo, hi);
+      if (lane == 0) parts[warp] = p;
+      __syncwarp();
+    }
     for (long long x = lo; x < hi;) {
       float m = -INFINITY, l = 0.f, mv = -INFINITY;
       int n;  // this group's steps here
       {
-        const PrePart p = part_of(x);
-        __syncwarp();
-        if (lane == 0) parts[warp] = p;  // for the end of the part
+        const PrePart p = parts[warp];
         const int nq = snq[p.b], pos0 = slen[p.b] - nq;
         const int rr = p.r0 + gr * 128 + row;
         const bool valid = rr < nq * a.G;
@@ -392,42 +430,50 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         n = min(p.j1, p.ntile(gr)) - p.j0;
         const uint32_t steps = max(0, min(p.j1, max(p.nt0, p.nt1)) - p.j0);
         if (n > 0) {
-        // ---- the warp's 32 rows of q, one after the other (whole rows at a
-        // time): fp16, the largest element in [2^14, 2^15)
-        float fcol = 0.f;
+        // ---- q: the warp copies its 32 rows as they are to where they belong
+        // (two rows at a time, chunks of 16 bytes turned by the row), each
+        // thread then turns its own row into fp16 with its largest element in
+        // [2^14, 2^15)
+        float fcol;
         {
-          const int w0 = p.r0 + gr * 128 + (row & ~31), R = nq * a.G;
-          const float sgn = a.scale < 0.f ? -1.f : 1.f;
-          int tk = w0 / a.G, hd = w0 - tk * a.G;
-          const __nv_bfloat16* src = a.q + p.b * a.qs + (long long)(p.h * a.G) * a.qh + 4 * lane;
-#pragma unroll 1
-          for (int i0 = 0; i0 < 32; i0 += 8) {
-            uint2 w[8];
+          const int w0 = row & ~31, R = nq * a.G, ch = lane & 15;
+          int r = p.r0 + gr * 128 + w0 + (lane >> 4);
+          int tk = r / a.G, hd = r - tk * a.G;
+          const __nv_bfloat16* src = a.q + p.b * a.qs + (long long)(p.h * a.G) * a.qh + 8 * ch;
+#pragma unroll 4
+          for (int i = 0; i < 32; i += 2) {
+            const int rw = w0 + i + (lane >> 4);
+            cp_async16(qs + (ch >> 3) * kQHalf + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4),
+                       r < R ? src + (long long)hd * a.qh + (long long)tk * a.qt : a.q, r < R ? 16 : 0);
+            r += 2;
+            for (hd += 2; hd >= a.G; hd -= a.G) ++tk;
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          __syncwarp();
+          uint8_t* mine = qs + row * 128;
+          uint32_t mx = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              w[i] = w0 + i0 + i < R
-                         ? __ldg(reinterpret_cast<const uint2*>(src + (long long)hd * a.qh + (long long)tk * a.qt))
-                         : make_uint2(0, 0);
-              if (++hd == a.G) {
-                hd = 0;
-                ++tk;
-              }
-            }
+          for (int i = 0; i < 16; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4*>(mine + (i >> 3) * kQHalf + (((i & 7) ^ (row & 7)) << 4));
+            mx = __vmaxu2(mx, w.x & 0x7fff7fffu);
+            mx = __vmaxu2(mx, w.y & 0x7fff7fffu);
+            mx = __vmaxu2(mx, w.z & 0x7fff7fffu);
+            mx = __vmaxu2(mx, w.w & 0x7fff7fffu);
+          }
+          mx = max(mx >> 16, mx & 0xffffu);
+          int e = (int)(mx >> 7) - 127;
+          e = mx == 0 || e == 128 ? 14 : max(e, -100);
+          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23) * (a.scale < 0.f ? -1.f : 1.f);
+          fcol = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * (fabsf(a.scale) * kLog2e);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint32_t mx = __vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu);
-              mx = __reduce_max_sync(0xffffffffu, max(mx >> 16, mx & 0xffffu));
-              int e = (int)(mx >> 7) - 127;
-              e = mx == 0 || e == 128 ? 14 : max(e, -100);
-              const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23) * sgn;
-              if (lane == i0 + i)
-                fcol = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * (fabsf(a.scale) * kLog2e);
-              const int rw = (row & ~31) + i0 + i;
-              *reinterpret_cast<uint2*>(qs + (lane >> 4) * kQHalf + rw * 128 +
-                                        ((((lane & 15) >> 1) ^ (rw & 7)) << 4) + (lane & 1) * 8) =
-                  make_uint2(pack_h2(bf_lo(w[i].x) * up, bf_hi(w[i].x) * up),
-                             pack_h2(bf_lo(w[i].y) * up, bf_hi(w[i].y) * up));
-            }
+          for (int i = 0; i < 16; ++i) {
+            uint4* at = reinterpret_cast<uint4*>(mine + (i >> 3) * kQHalf + (((i & 7) ^ (row & 7)) << 4));
+            const uint4 w = *at;
+            *at = make_uint4(pack_h2(bf_lo(w.x) * up, bf_hi(w.x) * up),
+                             pack_h2(bf_lo(w.y) * up, bf_hi(w.y) * up),
+                             pack_h2(bf_lo(w.z) * up, bf_hi(w.z) * up),
+                             pack_h2(bf_lo(w.w) * up, bf_hi(w.w) * up));
           }
         }
         fence_proxy_async_smem();
@@ -529,8 +575,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         done += steps;
       }
       // ---- the row's sums (no registers for its place in the loop above)
-      __syncwarp();
-      const PrePart p = parts[warp];
+      PrePart p = parts[warp];
+      if (p.j1 > p.j0) {
       float4* records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.ws) + pre_records(gridDim.x));
       const bool whole = p.j0 == 0 && p.j1 == p.steps;
       const float4 st = make_float4(m, l, mv, 0.f);
@@ -574,6 +620,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
                             __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
         }
       }
+      if (n > 0) {
+        tc_fence_before();
+        mbar_arrive(&oempty[gr]);
+      }
       if (whole) {
         __syncwarp();
         // two whole rows of the warp's 32 at a time
@@ -591,10 +641,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           for (hd += 2; hd >= a.G; hd -= a.G) ++tk;
         }
       }
-      if (n > 0) {
-        tc_fence_before();
-        mbar_arrive(&oempty[gr]);
-      }
       if (!whole) {
         rec[0] = st;
         // a tile that begins in this CTA and goes on in others: for the merge
@@ -602,7 +648,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           cuts[blockIdx.x] = make_int4(p.b, p.h, p.r0,
                                        (int)(((p.first + p.steps) * C - 1) / total));
       }
-      x = p.first + p.j1;
+      }
+      advance(p, x);
+      __syncwarp();
+      if (lane == 0) parts[warp] = p;
+      __syncwarp();
     }
   } else if (warp < 12) {
     // ================ converters
@@ -670,8 +720,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       return __reduce_max_sync(0xffffffffu, mx);
     };
     bool live = true;
-    for (long long x = lo; x < hi && live;) {
-      const PrePart p = part_of(x);
+    PrePart p;
+    if (lo < hi) p = find_part(line, lo, hi);
+    for (long long x = lo; x < hi && live; advance(p, x)) {
       const int L = slen[p.b], last = max(p.nt0, p.nt1);
       const int j1 = min(p.j1, last);
       if (p.j0 < j1) {
@@ -766,7 +817,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         mbar_arrive(&vfull[buf]);
         ++cnt;
       }
-      x = p.first + p.j1;
     }
   } else {
     // ================ products
@@ -778,8 +828,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       // parts
       uint32_t cnt = 0, np0 = 0, np1 = 0, ns0 = 0, ns1 = 0;
       bool live = true;
-      for (long long x = lo; x < hi && live;) {
-        const PrePart p = part_of(x);
+      PrePart p;
+      if (lo < hi) p = find_part(line, lo, hi);
+      for (long long x = lo; x < hi && live; advance(p, x)) {
         const int j1 = min(p.j1, max(p.nt0, p.nt1)), n = max(0, j1 - p.j0);
         // the groups' steps here
         const int n0 = max(0, min(p.j1, p.nt0) - p.j0), n1 = max(0, min(p.j1, p.nt1) - p.j0);
@@ -850,7 +901,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         cnt += n;
         if (n0 > 0) { np0 ^= (((n0 + 1) >> 1) & 1) | (((n0 >> 1) & 1) << 1); ++ns0; }
         if (n1 > 0) { np1 ^= (((n1 + 1) >> 1) & 1) | (((n1 >> 1) & 1) << 1); ++ns1; }
-        x = p.first + p.j1;
       }
       // every product has ended before TMEM is freed
       if (works && elect_one()) {
