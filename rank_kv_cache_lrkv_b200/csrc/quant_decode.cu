@@ -159,6 +159,12 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
   const long long lo = total * blockIdx.x / C, hi = total * (blockIdx.x + 1) / C;
 
   // the part that block x of the line belongs to, cut to [lo, hi)
+  auto groups_of = [&](int b) { return (snq[b] * a.G + kRows - 1) / kRows; };
+  auto cut = [&](Part& p) {
+    p.tiles = max(1, (slen[p.b] + kQBlock - 1) / kQBlock);
+    p.i0 = (int)max(0ll, lo - p.first);
+    p.i1 = (int)(min(hi, p.first + p.tiles) - p.first);
+  };
   auto part_of = [&](long long x) {
     Part p;
     int l = 0, r = c.B;
@@ -167,16 +173,25 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
       if (start[mid] <= x) l = mid; else r = mid;
     }
     p.b = l;
-    p.tiles = max(1, (slen[l] + kQBlock - 1) / kQBlock);
-    const int groups = (snq[l] * a.G + kRows - 1) / kRows;
-    const long long in = x - start[l];
-    const int u = (int)(in / p.tiles);
+    const int tiles = max(1, (slen[l] + kQBlock - 1) / kQBlock), groups = groups_of(l);
+    const int u = (int)((x - start[l]) / tiles);
     p.h = u / groups;
     p.rg = u - p.h * groups;
-    p.first = start[l] + (long long)u * p.tiles;
-    p.i0 = (int)(max(lo, p.first) - p.first);
-    p.i1 = (int)(min(hi, p.first + p.tiles) - p.first);
+    p.first = start[l] + (long long)u * tiles;
+    cut(p);
     return p;
+  };
+  // the part after p, whose first block is the line's block p.first + p.tiles
+  auto next_part = [&](Part& p) {
+    p.first += p.tiles;
+    if (++p.rg == groups_of(p.b)) {
+      p.rg = 0;
+      if (++p.h == c.H) {
+        p.h = 0;
+        do ++p.b; while (start[p.b + 1] == start[p.b]);
+      }
+    }
+    cut(p);
   };
 
   // ---------------- consumer: the loads it has in flight
@@ -185,14 +200,14 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
   int n_issued = 0, n_read = 0;      // slabs asked for, slabs used
   uint32_t bad = 0;                  // stages whose page was out of range
   long long xi = lo + warp;          // next block to ask for
-  Part pi;                           // its part (the last one looked up)
-  if (warp < W && xi < hi) pi = part_of(xi);
+  const Part p0 = part_of(lo);
+  Part pi = p0;                      // its part
   // next full block at or after xi; its page id is loaded here and first
   // looked at by the issue() after this one
   int npage = -1, nhead = 0;
   auto find_next = [&]() {
     while (xi < hi) {
-      if (xi >= pi.first + pi.i1) pi = part_of(xi);
+      while (xi >= pi.first + pi.tiles) next_part(pi);
       const int i = (int)(xi - pi.first);
       if ((i + 1) * kQBlock <= slen[pi.b]) {
         npage = __ldg(c.bt + (size_t)pi.b * c.maxp + i);
@@ -228,15 +243,15 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
   };
   if (warp < W) {
     more = find_next();
-#pragma unroll
+#pragma unroll 1
     for (int s = 0; s < D; ++s) issue();
   }
 
   int* counters = static_cast<int*>(a.ws);
   float* records = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + dec_records(gridDim.x));
 
+  Part p = p0;
   for (long long x = lo; x < hi;) {
-    const Part p = part_of(x);
     const int L = slen[p.b], nq = snq[p.b], R = nq * a.G;
     const int r0 = p.rg * kRows, rows = min(kRows, R - r0);
     const int pos0 = L - nq;  // position of query 0
@@ -658,6 +673,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
       }
     }
     x = p.first + p.i1;
+    if (x < hi) next_part(p);
   }
   if (*fail) {
     // copies still landing end before the CTA does
@@ -701,8 +717,15 @@ int quant_attn_launch(const QuantAttnArgs& a, cudaStream_t st) {
   DevInfo info;
   const int rc = current_device_info(dev, info);
   if (rc != LRKV_OK) return rc;
-  if ((long long)a.n * a.G <= 8)
+  // Six consumer warps with two slabs each: one token of the 32K layer (G 4)
+  // 51.7 us, 64 sequences of 12000 239 us (6,576 GB/s); five warps 58.0 and
+  // 269, eight with one slab each 57.1 and 261, four with three 53.9 and 254.
+  // More sequences than the lengths' place in shared memory allows: five.
+  if ((long long)a.n * a.G <= 8) {
+    if (dec_plan(6, 2, 8, a.c.B).total <= info.optin)
+      return a.c.e4m3 ? launch<true, 1, 6, 2>(a, info, st) : launch<false, 1, 6, 2>(a, info, st);
     return a.c.e4m3 ? launch<true, 1, 5, 2>(a, info, st) : launch<false, 1, 5, 2>(a, info, st);
+  }
   if ((long long)a.n * a.G <= kMaxRows)
     return a.c.e4m3 ? launch<true, 2, 4, 2>(a, info, st) : launch<false, 2, 4, 2>(a, info, st);
   return quant_prefill_launch(a, info, st);
