@@ -11,8 +11,9 @@
 // most 2^14 whatever the blocks' scales, are rounded to fp16 once and keep
 // eleven bits down to 2^-27 of the largest.
 //
-// One launch, persistent, one CTA per SM.  The blocks of all (unit, row
-// group)s are laid end to end and each CTA takes an equal contiguous range.
+// One launch, persistent, one CTA per SM.  The blocks of all units are laid
+// end to end and each CTA takes an equal contiguous range (the caller keeps
+// batch x heads x pages under 2^31: the line is counted in 32 bits).
 //  * W consumer warps take every W-th block.  Each keeps D page slabs (codes
 //    and scales, one bulk copy each) of its own in flight and refills a stage
 //    as soon as it has read it, so no warp waits for another's page.
@@ -48,7 +49,7 @@ __host__ __device__ inline DecPlan dec_plan(int W, int D, int rows, int B) {
   p.ml = p.slots + (W + 1) * rows * kPad * 4;
   p.full = p.ml + (W + 1) * rows * 16;
   p.start = p.full + W * D * 8;
-  p.len = p.start + (B + 1) * 8;
+  p.len = p.start + (B + 1) * 4;
   p.nq = p.len + B * 4;
   p.misc = p.nq + B * 4;
   p.total = p.misc + 16;
@@ -100,8 +101,7 @@ __device__ __forceinline__ float col_sum(float v) {
 // A part of a unit: its place, the blocks [i0, i1) of `tiles` in this CTA's
 // range, and the line's index of its block 0.
 struct Part {
-  int b, h, rg, tiles, i0, i1;
-  long long first;
+  int b, h, tiles, i0, i1, first;
 };
 
 template <bool kE4M3, int NT, int W, int D>
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + pl.full);
   float* slots = reinterpret_cast<float*>(sm + pl.slots);
   float4* ml = reinterpret_cast<float4*>(sm + pl.ml);  // [W + 1][kRows] (m, l, M')
-  long long* start = reinterpret_cast<long long*>(sm + pl.start);
+  int* start = reinterpret_cast<int*>(sm + pl.start);
   int* slen = reinterpret_cast<int*>(sm + pl.len);
   int* snq = reinterpret_cast<int*>(sm + pl.nq);
   volatile int* fail = reinterpret_cast<volatile int*>(sm + pl.misc);
@@ -130,77 +130,77 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
     // blocks before each sequence; a sequence without tokens still has one
     // (empty) block for its queries' zeros
     const int per = (c.B + 31) / 32, b0 = min(c.B, lane * per), b1 = min(c.B, b0 + per);
-    long long own = 0;
+    int own = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       slen[b] = quant_len(c, b);
       snq[b] = quant_queries(a, b);
-      const int groups = (snq[b] * a.G + kRows - 1) / kRows;
-      own += (long long)max(1, (slen[b] + kQBlock - 1) / kQBlock) * groups * c.H;
+      if (snq[b]) own += max(1, (slen[b] + kQBlock - 1) / kQBlock) * c.H;
     }
-    long long incl = own;
+    int incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    long long e = incl - own;
+    int e = incl - own;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       start[b] = e;
-      const int groups = (snq[b] * a.G + kRows - 1) / kRows;
-      e += (long long)max(1, (slen[b] + kQBlock - 1) / kQBlock) * groups * c.H;
+      if (snq[b]) e += max(1, (slen[b] + kQBlock - 1) / kQBlock) * c.H;
     }
     if (lane == 31) start[c.B] = incl;
   }
   __syncthreads();
-  const long long total = start[c.B];
+  const int total = start[c.B];
   // no CTA without a block: the parts of a unit are counted as CTAs
-  const int C = (int)min((long long)gridDim.x, total);
+  const int C = min((int)gridDim.x, total);
   if ((int)blockIdx.x >= C) return;
-  const long long lo = total * blockIdx.x / C, hi = total * (blockIdx.x + 1) / C;
+  // CTA i takes per blocks, the first `extra` CTAs one more
+  const int per = total / C, extra = total - per * C;
+  auto range_lo = [&](int i) { return i * per + min(i, extra); };
+  auto cta_of = [&](int y) {
+    const int big = extra * (per + 1);
+    return y < big ? y / (per + 1) : extra + (y - big) / per;
+  };
+  const int lo = range_lo(blockIdx.x), hi = range_lo(blockIdx.x + 1);
 
-  // the part that block x of the line belongs to, cut to [lo, hi)
-  auto groups_of = [&](int b) { return (snq[b] * a.G + kRows - 1) / kRows; };
   auto cut = [&](Part& p) {
     p.tiles = max(1, (slen[p.b] + kQBlock - 1) / kQBlock);
-    p.i0 = (int)max(0ll, lo - p.first);
-    p.i1 = (int)(min(hi, p.first + p.tiles) - p.first);
-  };
-  auto part_of = [&](long long x) {
-    Part p;
-    int l = 0, r = c.B;
-    while (r - l > 1) {
-      const int mid = (l + r) >> 1;
-      if (start[mid] <= x) l = mid; else r = mid;
-    }
-    p.b = l;
-    const int tiles = max(1, (slen[l] + kQBlock - 1) / kQBlock), groups = groups_of(l);
-    const int u = (int)((x - start[l]) / tiles);
-    p.h = u / groups;
-    p.rg = u - p.h * groups;
-    p.first = start[l] + (long long)u * tiles;
-    cut(p);
-    return p;
+    p.i0 = max(0, lo - p.first);
+    p.i1 = min(hi - p.first, p.tiles);
   };
   // the part after p, whose first block is the line's block p.first + p.tiles
   auto next_part = [&](Part& p) {
     p.first += p.tiles;
-    if (++p.rg == groups_of(p.b)) {
-      p.rg = 0;
-      if (++p.h == c.H) {
-        p.h = 0;
-        do ++p.b; while (start[p.b + 1] == start[p.b]);
-      }
+    if (++p.h == c.H) {
+      p.h = 0;
+      do ++p.b; while (start[p.b + 1] == start[p.b]);
     }
     cut(p);
   };
+  // the part that the range begins with
+  Part p0;
+  {
+    int l = 0, r = c.B;
+#pragma unroll 1
+    while (r - l > 1) {
+      const int mid = (l + r) >> 1;
+      if (start[mid] <= lo) l = mid; else r = mid;
+    }
+    p0.b = l;
+    const int tiles = max(1, (slen[l] + kQBlock - 1) / kQBlock);
+    p0.h = (lo - start[l]) / tiles;
+    p0.first = start[l] + p0.h * tiles;
+    cut(p0);
+  }
 
   // ---------------- consumer: the loads it has in flight
   uint8_t* ring = sm + warp * D * kQSlab;
   uint64_t* bar = full + warp * D;
   int n_issued = 0, n_read = 0;      // slabs asked for, slabs used
   uint32_t bad = 0;                  // stages whose page was out of range
-  long long xi = lo + warp;          // next block to ask for
-  const Part p0 = part_of(lo);
+  int xi = lo + warp;                // next block to ask for
   Part pi = p0;                      // its part
   // next full block at or after xi; its page id is loaded here and first
   // looked at by the issue() after this one
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
   auto find_next = [&]() {
     while (xi < hi) {
       while (xi >= pi.first + pi.tiles) next_part(pi);
-      const int i = (int)(xi - pi.first);
+      const int i = xi - pi.first;
       if ((i + 1) * kQBlock <= slen[pi.b]) {
         npage = __ldg(c.bt + (size_t)pi.b * c.maxp + i);
         nhead = pi.h;
@@ -250,14 +250,19 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
   int* counters = static_cast<int*>(a.ws);
   float* records = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + dec_records(gridDim.x));
 
+  // r / G for r < 16
+  const uint32_t inv = (65536u + a.G - 1) / a.G;
+  auto query_of = [&](int r) { return (int)((r * inv) >> 16); };
+
   Part p = p0;
-  for (long long x = lo; x < hi;) {
-    const int L = slen[p.b], nq = snq[p.b], R = nq * a.G;
-    const int r0 = p.rg * kRows, rows = min(kRows, R - r0);
+  for (int x = lo; x < hi;) {
+    const int L = slen[p.b], nq = snq[p.b], rows = nq * a.G;  // at most kRows
     const int pos0 = L - nq;  // position of query 0
-    const int minpos = pos0 + r0 / a.G;
     const __nv_bfloat16* qb = a.q + p.b * a.qs + (long long)(p.h * a.G) * a.qh;
-    auto qrow = [&](int r) { return qb + (long long)(r % a.G) * a.qh + (long long)(r / a.G) * a.qt; };
+    auto qrow = [&](int r) {
+      const int i = query_of(r);
+      return qb + (long long)(r - i * a.G) * a.qh + (long long)i * a.qt;
+    };
     float m[2 * NT], l[2 * NT], mv[2 * NT], acc[8][NT][4];
     int pos[2 * NT];
 #pragma unroll
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
       l[i] = 0.f;
       // this lane's columns: row 8 (i / 2) + 2 t + i % 2
       const int r = 8 * (i >> 1) + 2 * t + (i & 1);
-      pos[i] = r < rows ? pos0 + (r0 + r) / a.G : 0x7fffffff;
+      pos[i] = r < rows ? pos0 + query_of(r) : 0x7fffffff;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -279,9 +284,9 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
 
     if (warp < W) {
       // ---------------- quantised blocks
-      long long xc = x + ((warp - (int)((x - lo) % W)) + W) % W;
-      const long long xend = p.first + p.i1;
-      const bool have = xc < xend && ((int)(xc - p.first) + 1) * kQBlock <= L;
+      int xc = x + ((warp - (x - lo) % W) + W) % W;
+      const int xend = p.first + p.i1;
+      const bool have = xc < xend && (xc - p.first + 1) * kQBlock <= L;
       if (have) {
         any = true;
         // q's B fragments, fp16, and the columns' factors
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
           if (r < rows) {
-            const uint4* src = reinterpret_cast<const uint4*>(qrow(r0 + r));
+            const uint4* src = reinterpret_cast<const uint4*>(qrow(r));
             w[0] = __ldg(src + 2 * t);
             w[1] = __ldg(src + 2 * t + 1);
             w[2] = __ldg(src + 8 + 2 * t);
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
           fcol[2 * n + 1] = __shfl_sync(0xffffffffu, down, 8 * t + 4) * (a.scale * kLog2e);
         }
         for (; xc < xend; xc += W) {
-          const int i = (int)(xc - p.first);
+          const int i = xc - p.first;
           if ((i + 1) * kQBlock > L) break;
           const int s = n_read % D;
           const bool ok = quant_wait_warp(&bar[s], (n_read / D) & 1, fail, lane);
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
             }
             // ---- softmax: one maximum per column and block
             const int base = i * kQBlock;
-            const bool edge = base + kQBlock - 1 > minpos;
+            const bool edge = base + kQBlock - 1 > pos0;
             float corr[2 * NT];
             bool moved = false;
             // s_v = 2^ev fv, 1 <= fv < 2 (a NaN stays in fv)
@@ -479,7 +484,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           qw[n] = 8 * n + g < rows
-                      ? __ldg(reinterpret_cast<const uint4*>(qrow(r0 + 8 * n + g)) + 4 * u4 + t)
+                      ? __ldg(reinterpret_cast<const uint4*>(qrow(8 * n + g)) + 4 * u4 + t)
                       : zero;
 #pragma unroll
         for (int s4 = 0; s4 < 4; ++s4) {
@@ -604,40 +609,42 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
       }
     __syncthreads();
     const bool whole = p.i0 == 0 && p.i1 == p.tiles;
-    // record of this unit's part in CTA cc (c0: the CTA that it begins in)
+    // record of this unit's part in CTA cc (begins: in that CTA)
     auto record = [&](int cc, bool begins) {
       return reinterpret_cast<float4*>(records + ((size_t)2 * cc + (begins ? 1 : 0)) * kMaxRows * kPad);
     };
     // a row's result, or zeros where it saw nothing: lane's 4 dims
     auto finish = [&](int r, const float4& st, const float4& o) {
-      const int rr = r0 + r;
-      __nv_bfloat16* dst = a.o + p.b * a.os + (long long)(p.h * a.G + rr % a.G) * a.oh +
-                           (long long)(rr / a.G) * a.ot + 4 * lane;
+      const int i = query_of(r);
+      __nv_bfloat16* dst = a.o + p.b * a.os + (long long)(p.h * a.G + r - i * a.G) * a.oh +
+                           (long long)i * a.ot + 4 * lane;
       const float f = st.y == 0.f ? 0.f : ex2_approx(st.z - st.x) / st.y;
       *reinterpret_cast<uint2*>(dst) =
           make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
     };
-    // fold one part's (st, s) into (S, o); a part that saw nothing (a NaN sum
-    // is something) adds nothing
-    auto fold = [&](float4& S, float4& o, const float4& st, const float4& s) {
-      if (st.x == -INFINITY && st.y == 0.f) return;
-      const float mn = fmaxf(S.x, st.x), ref = mn == -INFINITY ? 0.f : mn;
-      const float zn = fmaxf(S.z, st.z), zref = zn == -INFINITY ? 0.f : zn;
-      S.y = S.y * ex2_approx(S.x - ref) + st.y * ex2_approx(st.x - ref);
-      const float f0 = ex2_approx(S.z - zref), f1 = ex2_approx(st.z - zref);
-      S.x = mn;
-      S.z = zn;
-      o.x = o.x * f0 + s.x * f1;
-      o.y = o.y * f0 + s.y * f1;
-      o.z = o.z * f0 + s.z * f1;
-      o.w = o.w * f0 + s.w * f1;
-    };
-    const float4 none = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    // A part that saw nothing (a NaN sum is something) adds nothing.
+    auto nothing = [](const float4& st) { return st.x == -INFINITY && st.y == 0.f; };
+    auto zero_if_inf = [](float x) { return x == -INFINITY ? 0.f : x; };
     for (int r = warp; r < rows; r += W + 1) {
-      float4 S = none, o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w <= W; ++w)
-        fold(S, o, ml[w * kRows + r],
-             *reinterpret_cast<const float4*>(slots + ((size_t)w * kRows + r) * kPad + 4 * lane));
+      float4 st[W + 1], S = make_float4(-INFINITY, 0.f, -INFINITY, 0.f), o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w <= W; ++w) {
+        st[w] = ml[w * kRows + r];
+        S.x = fmaxf(S.x, st[w].x);
+        S.z = fmaxf(S.z, st[w].z);
+      }
+      const float ref = zero_if_inf(S.x), zref = zero_if_inf(S.z);
+#pragma unroll
+      for (int w = 0; w <= W; ++w) {
+        if (nothing(st[w])) continue;
+        const float f = ex2_approx(st[w].z - zref);
+        const float4 v = *reinterpret_cast<const float4*>(slots + (w * kRows + r) * kPad + 4 * lane);
+        S.y += st[w].y * ex2_approx(st[w].x - ref);
+        o.x += v.x * f;
+        o.y += v.y * f;
+        o.z += v.z * f;
+        o.w += v.w * f;
+      }
       if (whole) {
         finish(r, S, o);
       } else {
@@ -647,26 +654,38 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
       }
     }
     if (!whole) {
-      // CTAs that hold blocks of this unit: block y lies in CTA
-      // ((y + 1) C - 1) / total
-      const int c0 = (int)(((p.first + 1) * C - 1) / total);
-      const int c1 = (int)(((p.first + p.tiles) * C - 1) / total);
-      __threadfence();
+      // the CTAs that hold blocks of this unit; the barrier hands all threads'
+      // records to thread 0, whose atomic releases them and acquires the others'
+      const int c0 = cta_of(p.first), c1 = cta_of(p.first + p.tiles - 1);
       __syncthreads();
       if (threadIdx.x == 0) {
-        const int before = atomicAdd(&counters[c0], 1);
+        int before;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                     : "=r"(before)
+                     : "l"(counters + c0)
+                     : "memory");
         *lastflag = before == c1 - c0;
         if (before == c1 - c0) counters[c0] = 0;
       }
       __syncthreads();
       if (*lastflag) {
-        __threadfence();
         for (int r = warp; r < rows; r += W + 1) {
-          float4 S = none, o = make_float4(0.f, 0.f, 0.f, 0.f);
+          float4 S = make_float4(-INFINITY, 0.f, -INFINITY, 0.f), o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
           for (int cc = c0; cc <= c1; ++cc) {
             const float4* src = record(cc, cc == c0) + r * (kPad / 4);
-            fold(S, o, __ldcg(src), __ldcg(src + 1 + lane));
+            const float4 v = __ldcg(src), u = __ldcg(src + 1 + lane);
+            if (nothing(v)) continue;
+            const float mn = fmaxf(S.x, v.x), zn = fmaxf(S.z, v.z);
+            const float ref = zero_if_inf(mn), zref = zero_if_inf(zn);
+            S.y = S.y * ex2_approx(S.x - ref) + v.y * ex2_approx(v.x - ref);
+            const float f0 = ex2_approx(S.z - zref), f1 = ex2_approx(v.z - zref);
+            S.x = mn;
+            S.z = zn;
+            o.x = o.x * f0 + u.x * f1;
+            o.y = o.y * f0 + u.y * f1;
+            o.z = o.z * f0 + u.z * f1;
+            o.w = o.w * f0 + u.w * f1;
           }
           finish(r, S, o);
         }

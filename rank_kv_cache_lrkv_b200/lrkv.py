@@ -441,6 +441,7 @@ class QuantCache:
         self.pages = torch.zeros((self.num_pages, H_kv, QUANT_SLAB_BYTES), dtype=torch.uint8,
                                  device=device)
         self.device = self.pages.device
+        self.device_index = self.pages.get_device()  # -1: not on a GPU
         ids = torch.arange(self.num_pages, dtype=torch.int32) if page_perm is None else \
             torch.as_tensor(page_perm, dtype=torch.int32)
         self.block_table = ids.reshape(B, self.max_pages).to(device)
@@ -467,7 +468,7 @@ def _quant_rows(name: str, cache: QuantCache, x: torch.Tensor, heads: int, dtype
     sh = x.shape
     if len(sh) != 4 or sh[0] != cache.B or sh[1] != heads or sh[3] != HEAD_DIM:
         raise ValueError(f"{name} must be [{cache.B}, {heads}, n, {HEAD_DIM}], not {list(sh)}")
-    if x.dtype != dtype or x.device != cache.device:
+    if x.dtype != dtype or x.get_device() != cache.device_index:
         raise ValueError(f"{name} must be {dtype} on {cache.device}, not {x.dtype} on {x.device}")
     st = x.stride()
     if st[3] != 1:
@@ -484,8 +485,8 @@ def _quant_written(name: str, x: torch.Tensor, st):
 def _quant_counts(name: str, cache: QuantCache, t: Optional[torch.Tensor]):
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != cache.device or t.shape != (cache.B,) or \
-            not t.is_contiguous():
+    if t.dtype != torch.int32 or t.get_device() != cache.device_index or \
+            t.shape != (cache.B,) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 [{cache.B}] on {cache.device}")
     return t.data_ptr()
 
@@ -493,17 +494,17 @@ def _quant_counts(name: str, cache: QuantCache, t: Optional[torch.Tensor]):
 def _quant_call(name: str, cache: QuantCache, stream, *args) -> None:
     """Run an entry point on the cache's device, on `stream` or that device's
     current stream."""
-    dev = cache.device
-    if dev.type != "cuda":
-        raise ValueError(f"the cache is on {dev}, not on a CUDA device")
+    dev = cache.device_index
+    if dev < 0:
+        raise ValueError(f"the cache is on {cache.device}, not on a CUDA device")
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    elif stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the cache on {dev}")
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device != cache.device:
+        raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
     else:
         raw = stream.cuda_stream
     fn = getattr(_lib, name)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev:
         rc = fn(cache.desc_ref, *args, raw)
     else:
         with torch.cuda.device(dev):
@@ -569,7 +570,7 @@ def quant_attn(cache: QuantCache, q: torch.Tensor, scale: float, o: torch.Tensor
     qp, op = q4.data_ptr(), o4.data_ptr()
     if qp == op and qp:
         raise ValueError("o may not be q: q is read while o is written")
-    if workspace.device != cache.device or not workspace.is_contiguous() or \
+    if workspace.get_device() != cache.device_index or not workspace.is_contiguous() or \
             workspace.dtype != torch.uint8:
         raise ValueError(f"workspace must be contiguous uint8 on {cache.device}")
     _quant_call("lrkv_quant_attn", cache, stream, qp, heads, sh[2],

@@ -96,6 +96,8 @@ def test_attention_refuses_bad_calls(lrkv):
     assert call(hq=3) == -1 and call(hq=0) == -1 and call(n=-1) == -1
     assert call(hq=258) == -2                       # 129 query heads per KV head
     assert call(n=1 << 30) == -2                    # rows past 32 bits
+    many = ctypes.byref(_desc(lrkv, batch=1024, max_pages_per_seq=1 << 20))
+    assert call(desc=many) == -2                    # blocks past 32 bits
     assert call(n=0) == 0
     assert call(q=None) == -1 and call(o=None) == -1 and call(ws=None) == -1
     assert call(q=ODD) == -1 and call(o=ODD) == -1 and call(ws=ODD) == -1
