@@ -46,6 +46,16 @@ __host__ __device__ __forceinline__ int quant_k_chunk(int t, int ch) {
   return t * kHeadDim + ((ch ^ ((t & 1) << 2)) << 4);
 }
 
+// a + b on two fp32 lanes at once.
+__device__ __forceinline__ float2 add2(const float2 a, const float2 b) {
+  unsigned long long dd, aa, bb;
+  memcpy(&aa, &a, 8); memcpy(&bb, &b, 8);
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(dd) : "l"(aa), "l"(bb));
+  float2 d;
+  memcpy(&d, &dd, 8);
+  return d;
+}
+
 // Value of a stored byte.
 template <bool kE4M3>
 __device__ __forceinline__ float quant_value(uint32_t byte) {

@@ -15,7 +15,7 @@ int check_quant(const lrkv_quant_cache* c) {
   if (c->code != LRKV_CODE_INT8 && c->code != LRKV_CODE_E4M3) return LRKV_ERR_UNSUPPORTED;
   if (c->head_dim != kHeadDim) return LRKV_ERR_UNSUPPORTED;
   if (c->batch < 1 || c->batch > LRKV_MAX_BATCH || c->num_kv_heads < 1 ||
-      c->num_kv_heads > 65535)
+      c->num_kv_heads > 32767)
     return LRKV_ERR_ARG;
   // positions are 32-bit
   if (c->num_pages < 1 || c->max_pages_per_seq < 1 || c->max_pages_per_seq > INT_MAX / kQBlock - 2)

@@ -3,15 +3,16 @@
 // Append: a = max |x| over the 64 x 128 values of a block, s = a / M, code =
 // rne(M x / a), M = 127 (whole numbers) or 448 (e4m3).  The codes are those
 // of exact arithmetic, without a division per value:
-//  * y = x * (M / a) in fp32 is off by at most 2^-22.9 of itself;
-//  * with x = X 2^p, a = A 2^r (X, A whole, below 256, p <= r) the quotient Q
-//    = M x / a is either a midpoint of two codes or at least 2^-16 of itself
-//    away from every midpoint.  int8, midpoint m / 2 (m odd): Q - m / 2 =
-//    (254 X 2^p - m A 2^r) / (2 A 2^r), a whole number of 2^p / (2 A 2^r) =
-//    Q / (254 X).  e4m3, midpoint m 2^t (m < 32): the same way at least
-//    Q / (7 X) or Q / (m A);
-//  * so y rounded to 19 bits (which moves it by at most 2^-19) is the
-//    midpoint itself where Q is one, and lies on Q's side of it otherwise.
+//  * M / a is held as r + q, r = M fl(1 / a) and q = (M - r a) fl(1 / a) (the
+//    remainder is exact: r a has 32 bits), so y = fl(x r + fl(x q)) is the
+//    quotient Q = M x / a off by less than 2^-26 of itself, then rounded once;
+//  * with x = X 2^p, a = A 2^e (X, A whole, below 256, p <= e) Q is either a
+//    midpoint of two codes or at least 2^-16 of itself away from every one.
+//    int8, midpoint m / 2 (m odd): Q - m / 2 = (254 X 2^p - m A 2^e) /
+//    (2 A 2^e), a whole number of 2^p / (2 A 2^e) = Q / (254 X).  e4m3,
+//    midpoint m 2^t (m < 32): the same way at least Q / (7 X) or Q / (m A);
+//  * a midpoint has 8 bits at most, so where Q is one, y is Q; elsewhere y
+//    lies on Q's side of it.
 #include "quant.cuh"
 
 namespace lrkv {
@@ -19,6 +20,9 @@ namespace lrkv {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendCtas = 4;  // resident per SM
+constexpr int kAhead = 2;       // blocks in flight per CTA
+constexpr int kAppendSmem = kAhead * 4 * kAppendThreads * 16 + 2 * kQSide;
 
 __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) {
   return __vmaxu2(m, w & 0x7fff7fffu);
@@ -27,33 +31,28 @@ __device__ __forceinline__ uint32_t abs_max8(uint32_t m, const uint4& w) {
   return abs_max2(abs_max2(abs_max2(abs_max2(m, w.x), w.y), w.z), w.w);
 }
 
-// x r rounded to 19 bits (r = M / a): Veltkamp's splitting, 24 - 5 bits.
-__device__ __forceinline__ float quant_scaled(float x, float r) {
-  const float y = __fmul_rn(x, r), z = __fmul_rn(y, 33.f);
-  return __fsub_rn(z, __fsub_rn(z, y));
-}
-// Two values' stored bytes (low byte: lo).
+// Eight values' stored bytes; rq = (r, q).  A whole number up to 127 is the
+// low byte of y + 1.5 2^23 + 128 (the sum rounds half to even).
 template <bool kE4M3>
-__device__ __forceinline__ uint32_t quant_code2(float lo, float hi, float r) {
-  const float x = quant_scaled(lo, r), y = quant_scaled(hi, r);
-  if constexpr (kE4M3) {
-    uint32_t w;
-    asm("{\n\t.reg .b16 p;\n\tcvt.rn.satfinite.e4m3x2.f32 p, %1, %2;\n\tcvt.u32.u16 %0, p;\n\t}"
-        : "=r"(w)
-        : "f"(y), "f"(x));
-    return w;
-  } else {
-    return (uint32_t)(__float2int_rn(x) + 128) | ((uint32_t)(__float2int_rn(y) + 128) << 8);
+__device__ __forceinline__ uint2 quant_code8(const uint4& w, float2 rq) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  const float2 r = make_float2(rq.x, rq.x), q = make_float2(rq.y, rq.y);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = bf2(in[i]);
+    float2 y = mul2(x, q);
+    fma2(y, x, r);
+    if constexpr (kE4M3) {
+      asm("{\n\t.reg .b16 p;\n\tcvt.rn.satfinite.e4m3x2.f32 p, %1, %2;\n\tcvt.u32.u16 %0, p;\n\t}"
+          : "=r"(c[i])
+          : "f"(y.y), "f"(y.x));
+    } else {
+      y = add2(y, make_float2(12583040.f, 12583040.f));
+      c[i] = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040);
+    }
   }
-}
-// The 8 bytes of 8 values.
-template <bool kE4M3>
-__device__ __forceinline__ uint2 quant_code8(const uint4& w, float r) {
-  const uint32_t p = quant_code2<kE4M3>(bf_lo(w.x), bf_hi(w.x), r);
-  const uint32_t q = quant_code2<kE4M3>(bf_lo(w.y), bf_hi(w.y), r);
-  const uint32_t u = quant_code2<kE4M3>(bf_lo(w.z), bf_hi(w.z), r);
-  const uint32_t s = quant_code2<kE4M3>(bf_lo(w.w), bf_hi(w.w), r);
-  return make_uint2(p | (q << 16), u | (s << 16));
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
 // 4 x 4 byte transpose: word i of the result holds byte i of a, b, c, d.
@@ -67,23 +66,29 @@ __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, u
   r[3] = __byte_perm(ab1, cd1, 0x7632);
 }
 
-// One CTA per (block that the call touches, KV head, sequence).
-//  * A block that becomes full: thread (token, 16-byte chunk) holds the key
-//    rows, thread (4 tokens, chunk) the value rows (so that its codes
-//    transpose in registers); maximum over the CTA; codes into shared memory
-//    in the slab's layout; one bulk store.
+// CTAs (x, KV head and side, sequence); a CTA takes every gridDim.x-th block
+// that the call touches.  A thread's chunks of the next kAhead blocks arrive
+// by cp.async in places of its own: no barrier for them, no bank conflicts,
+// and more bytes in flight than registers would hold.
+//  * A block that becomes full: a thread holds one 16-byte chunk of four
+//    tokens (16 apart for keys, consecutive for values: their codes transpose
+//    in registers); maximum over the CTA; the key codes go straight to their
+//    rows, the value codes turn through shared memory, 16-byte chunks of a
+//    row moved by its number against bank conflicts.
 //  * The rows of the call that the tail keeps (the open block and the one
 //    before it) are copied by the CTA of the first block, after it has read
 //    the open block's old rows: they may take those rows' slots.
 // The last CTA of a sequence to finish advances seq_len.
 template <bool kE4M3>
-__global__ void __launch_bounds__(kAppendThreads) quant_append_kernel(QuantAppendArgs a) {
-  __shared__ __align__(128) uint8_t slab[kQSlab];
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas) quant_append_kernel(QuantAppendArgs a) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  uint4* ring = reinterpret_cast<uint4*>(sm);  // [kAhead][4][threads]
+  uint8_t* codes0 = sm + kAhead * 4 * kAppendThreads * 16;  // [2][kQSide], values only
   __shared__ uint32_t part[2][kAppendThreads / 32];
   pdl_trigger();
   pdl_wait();
   const QuantView& c = a.c;
-  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y >> 1, side = blockIdx.y & 1, b = blockIdx.z, tid = threadIdx.x;
   const int L0 = quant_len(c, b);
   int n = a.n;
   if (a.n_new) n = max(0, min(n, a.n_new[b]));
@@ -91,99 +96,123 @@ __global__ void __launch_bounds__(kAppendThreads) quant_append_kernel(QuantAppen
   const bool over = L0 + (long long)n > cap;
   if (over) n = (int)(cap - L0);
   const int L1 = L0 + n;
-  const int j = L0 / kQBlock + blockIdx.x;
-  const __nv_bfloat16* krow = a.k + b * a.ss + h * a.hs;
-  const __nv_bfloat16* vrow = a.v + b * a.ss + h * a.hs;
-  // row of token t: the tail's for tokens of earlier calls
-  auto src = [&](int side, int t) {
-    return t < L0 ? quant_tail(c, b, h, side, t)
-                  : (side ? vrow : krow) + (long long)(t - L0) * a.ts;
+  const __nv_bfloat16* rows = (side ? a.v : a.k) + b * a.ss + h * a.hs;
+  // keys: tokens tid / 16 + 16 i, values: tokens 4 (tid / 16) + i; dims 8 d8 ..
+  const int t0 = side ? 4 * (tid >> 4) : tid >> 4, ts = side ? 1 : 16, d8 = tid & 15;
+  const int end = n > 0 ? L1 / kQBlock : 0;  // the first block that stays open
+  int j = L0 / kQBlock + blockIdx.x, it = 0, s = 0;
+  // this thread's first chunk of block j, and the way to its others
+  const __nv_bfloat16* src = rows + ((long long)j * kQBlock + t0 - L0) * a.ts + d8 * 8;
+  const long long step = (long long)ts * a.ts, jump = (long long)gridDim.x * kQBlock * a.ts;
+  const uint32_t mine = smem_u32(ring + tid);
+  int ask = j;  // the next block to ask for
+  auto load = [&](int st) {
+    if (ask < end) {
+      const uint32_t to = mine + st * (4 * kAppendThreads * 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat16* p = src + i * step;
+        // the open block's rows of earlier calls are the tail's
+        if (ask * kQBlock < L0) {
+          const int t = ask * kQBlock + t0 + ts * i;
+          if (t < L0) p = quant_tail(c, b, h, side, t) + d8 * 8;
+        }
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * kAppendThreads * 16),
+                     "l"(p)
+                     : "memory");
+      }
+    }
+    cp_async_commit();
+    ask += gridDim.x;
+    src += jump;
   };
-  const bool full = n > 0 && (long long)(j + 1) * kQBlock <= L1;
-  uint8_t* out = nullptr;
-  if (full) {
-    out = quant_slab(c, b, h, j);
-    if (!out && tid == 0) quant_error(c, kErrBadPage);
+#pragma unroll 1
+  for (int i = 0; i < kAhead; ++i) load(i);
+  if (blockIdx.x == 0 && n > 0) {
+    cp_async_wait<0>();
+    __syncthreads();  // the open block's old rows are read
+    // the call's rows that the tail keeps, 16 threads a row; all loads of a
+    // round in flight at once
+    const int k0 = max(L0, (L1 / kQBlock - 1) * kQBlock), e = (tid & 15) * 8;
+    for (int r0 = k0 + (tid >> 4); r0 < L1; r0 += 64) {
+      uint4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (r0 + 16 * i < L1)
+          w[i] = *reinterpret_cast<const uint4*>(rows + (long long)(r0 + 16 * i - L0) * a.ts + e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (r0 + 16 * i < L1)
+          *reinterpret_cast<uint4*>(quant_tail(c, b, h, side, r0 + 16 * i) + e) = w[i];
+    }
+    if (over && tid == 0) quant_error(c, kErrCapacity);
   }
-  if (over && tid == 0) quant_error(c, kErrCapacity);
-
-  uint4 kx[4], vx[4];
-  if (full) {  // uniform over the CTA
+#pragma unroll 1
+  for (; j < end; j += gridDim.x, it ^= 1) {
+    const int pg = __ldg(c.bt + (size_t)b * c.maxp + j);
+    uint8_t* codes = codes0 + it * kQSide;
+    cp_async_wait<kAhead - 1>();
+    uint4 x[4];
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      kx[i] = *reinterpret_cast<const uint4*>(src(0, j * kQBlock + (tid >> 4) + 16 * i) + (tid & 15) * 8);
-      vx[i] = *reinterpret_cast<const uint4*>(src(1, j * kQBlock + 4 * (tid & 15) + i) + (tid >> 4) * 8);
+      x[i] = ring[(s * 4 + i) * kAppendThreads + tid];
+      m = abs_max8(m, x[i]);
     }
-    uint32_t mk = 0, mv = 0;
+    load(s);
+    s = s + 1 == kAhead ? 0 : s + 1;
+    m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
+    if ((tid & 31) == 0) part[it][tid >> 5] = m;
+    __syncthreads();
+    m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      mk = abs_max8(mk, kx[i]);
-      mv = abs_max8(mv, vx[i]);
-    }
-    mk = max(mk >> 16, mk & 0xffffu);
-    mv = max(mv >> 16, mv & 0xffffu);
-    mk = __reduce_max_sync(0xffffffffu, mk);
-    mv = __reduce_max_sync(0xffffffffu, mv);
-    if (lane == 0) {
-      part[0][warp] = mk;
-      part[1][warp] = mv;
-    }
-  }
-  __syncthreads();
-  if (full && out) {
-    uint32_t mk = 0, mv = 0;
-#pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) {
-      mk = max(mk, part[0][w]);
-      mv = max(mv, part[1][w]);
-    }
-    const bool kbad = mk >= 0x7f80u, vbad = mv >= 0x7f80u;  // an infinity or a NaN
+    for (int w = 0; w < kAppendThreads / 32; ++w) m = max(m, part[it][w]);
+    const bool bad = m >= 0x7f80u;  // an infinity or a NaN
     const float top = kE4M3 ? 448.f : 127.f, least = 7.888609052210118e-31f;  // 2^-100
-    const float ak = fmaxf(__uint_as_float(mk << 16), least);
-    const float av = fmaxf(__uint_as_float(mv << 16), least);
-    const float rk = __fdiv_rn(top, ak), rv = __fdiv_rn(top, av);
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = (tid >> 4) + 16 * i, d8 = tid & 15;
-      *reinterpret_cast<uint2*>(slab + quant_k_chunk(t, d8 >> 1) + (d8 & 1) * 8) =
-          quant_code8<kE4M3>(kbad ? zero : kx[i], kbad ? 1.f : rk);
-    }
+    const float am = bad ? 1.f : fmaxf(__uint_as_float(m << 16), least);
+    const float inv = __frcp_rn(am);
+    float2 rq;
+    rq.x = top * inv;
+    rq.y = __fmaf_rn(-rq.x, am, top) * inv;
     uint2 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = quant_code8<kE4M3>(vbad ? zero : vx[i], vbad ? 1.f : rv);
-    uint32_t lo[4], hi[4];
-    transpose4(w[0].x, w[1].x, w[2].x, w[3].x, lo);
-    transpose4(w[0].y, w[1].y, w[2].y, w[3].y, hi);
-    uint32_t* vs = reinterpret_cast<uint32_t*>(slab + kQSide);
+    for (int i = 0; i < 4; ++i)
+      w[i] = quant_code8<kE4M3>(bad ? make_uint4(0, 0, 0, 0) : x[i], rq);
+    const bool there = pg >= 0 && pg < c.num_pages;
+    uint8_t* out = c.pages + ((size_t)(there ? pg : 0) * c.H + h) * kQSlab;
+    if (side == 0) {
+      if (there)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      vs[((tid >> 4) * 8 + i) * (kQBlock / 4) + (tid & 15)] = lo[i];
-      vs[((tid >> 4) * 8 + 4 + i) * (kQBlock / 4) + (tid & 15)] = hi[i];
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint2*>(out + quant_k_chunk(t0 + 16 * i, d8 >> 1) + (d8 & 1) * 8) = w[i];
+    } else {
+      uint32_t lo[4], hi[4];
+      transpose4(w[0].x, w[1].x, w[2].x, w[3].x, lo);
+      transpose4(w[0].y, w[1].y, w[2].y, w[3].y, hi);
+      // word tid / 16 of rows 8 d8 + i: chunk tid / 64 turned by d8
+      uint32_t* vs = reinterpret_cast<uint32_t*>(codes) + d8 * 8 * (kQBlock / 4) +
+                     ((((tid >> 6) ^ d8) & 3) << 2) + ((tid >> 4) & 3);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        vs[i * (kQBlock / 4)] = lo[i];
+        vs[(4 + i) * (kQBlock / 4)] = hi[i];
+      }
+      __syncthreads();
+      if (there)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int k = tid + i * kAppendThreads, d = k >> 2, ch = k & 3;  // row, chunk
+          reinterpret_cast<uint4*>(out + kQSide)[k] =
+              reinterpret_cast<const uint4*>(codes)[d * 4 + (ch ^ ((d >> 3) & 3))];
+        }
     }
-    if (tid < 8) {
-      const float nan = __uint_as_float(0x7fc00000u);
-      const float s = tid == 0 ? (kbad ? nan : __fdiv_rn(ak, top))
-                               : tid == 1 ? (vbad ? nan : __fdiv_rn(av, top)) : 0.f;
-      reinterpret_cast<float*>(slab + 2 * kQSide)[tid] = s;
-    }
-    proxy_fence_smem();
+    // the side's scale, and its half of the slab's zero bytes
+    float* sc = reinterpret_cast<float*>(out + 2 * kQSide);
+    if (there && tid == 0) sc[side] = bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(am, top);
+    if (there && tid >= 32 && tid < 35) sc[2 + 3 * side + tid - 32] = 0.f;
+    if (!there && tid == 0) quant_error(c, kErrBadPage);
   }
-  if (blockIdx.x == 0 && n > 0) {
-    // the call's rows that the tail keeps: 16 threads a row
-    const int t0 = max(L0, (L1 / kQBlock - 1) * kQBlock);
-    for (int i = tid; i < (L1 - t0) * 32; i += kAppendThreads) {
-      const int t = t0 + (i >> 5), side = (i >> 4) & 1, e = (i & 15) * 8;
-      *reinterpret_cast<uint4*>(quant_tail(c, b, h, side, t) + e) =
-          *reinterpret_cast<const uint4*>((side ? vrow : krow) + (long long)(t - L0) * a.ts + e);
-    }
-  }
-  __syncthreads();
   if (tid == 0) {
-    if (full && out) {
-      bulk_s2g(out, slab, kQSlab);
-      bulk_commit();
-    }
     // the last CTA of the sequence: every other has read seq_len
     __threadfence();
     const int last = (int)(gridDim.x * gridDim.y) - 1;
@@ -191,7 +220,6 @@ __global__ void __launch_bounds__(kAppendThreads) quant_append_kernel(QuantAppen
       c.seq_len[b] = L1;
       c.counter[b] = 0;
     }
-    if (full && out) bulk_wait<0>();
   }
 }
 
@@ -287,13 +315,21 @@ __global__ void __launch_bounds__(kAppendThreads) quant_read_kernel(QuantReadArg
 
 int quant_append_launch(const QuantAppendArgs& a, cudaStream_t st) {
   // blocks that n tokens can touch, wherever in a block they start
-  const unsigned nb = (unsigned)((a.n + 62ll) / kQBlock + 1);
-  const dim3 grid(nb, a.c.H, a.c.B);
+  const long long nb = (a.n + 62ll) / kQBlock + 1;
+  // no more CTAs than are resident at once: the rest is their loops' work
+  int dev = 0;
+  DevInfo info;
+  int rc = current_device_info(dev, info);
+  if (rc != LRKV_OK) return rc;
+  const long long room = (long long)info.sms * kAppendCtas / (2ll * a.c.H * a.c.B);
+  const dim3 grid((unsigned)(nb < room ? nb : room < 1 ? 1 : room), 2 * a.c.H, a.c.B);
   QuantAppendArgs args = a;
   void* p[] = {&args};
   const void* fn = a.c.e4m3 ? (const void*)quant_append_kernel<true>
                             : (const void*)quant_append_kernel<false>;
-  return launch_pdl(fn, grid, dim3(kAppendThreads), 0, st, p) == cudaSuccess ? LRKV_OK
+  rc = prepare_kernel(fn, true);
+  if (rc != LRKV_OK) return rc;
+  return launch_pdl(fn, grid, dim3(kAppendThreads), kAppendSmem, st, p) == cudaSuccess ? LRKV_OK
                                                                              : LRKV_ERR_CUDA;
 }
 

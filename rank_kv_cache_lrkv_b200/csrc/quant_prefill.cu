@@ -180,15 +180,6 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float2 add2(const float2 a, const float2 b) {
-  unsigned long long dd, aa, bb;
-  memcpy(&aa, &a, 8); memcpy(&bb, &b, 8);
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(dd) : "l"(aa), "l"(bb));
-  float2 d;
-  memcpy(&d, &dd, 8);
-  return d;
-}
-
 // The line, in shared memory: per sequence its start, what one KV head takes
 // of it, its length and its queries.
 struct Line {

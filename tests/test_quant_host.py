@@ -44,7 +44,7 @@ def test_struct_and_constants_match_the_header(lrkv, tmp_path):
 
 @pytest.mark.parametrize("field,value,status", [
     ("head_dim", 64, -2), ("code", 2, -2), ("code", -1, -2), ("batch", 0, -1), ("batch", 1025, -1),
-    ("num_kv_heads", 0, -1), ("num_kv_heads", 65536, -1), ("num_pages", 0, -1),
+    ("num_kv_heads", 0, -1), ("num_kv_heads", 32768, -1), ("num_pages", 0, -1),
     ("max_pages_per_seq", 0, -1), ("max_pages_per_seq", (1 << 25), -1), ("pages", 0, -1),
     ("pages", 8, -1), ("tail", 0, -1), ("tail", 24, -1), ("block_table", 0, -1),
     ("seq_len", 0, -1), ("append_counter", 0, -1), ("error", 0, -1)])
