@@ -189,6 +189,19 @@ def test_ragged_appends_and_ranges(lrkv, code):
                     assert np.array_equal(x[b, h].cpu().numpy(), want), (n, b, h, side)
 
 
+def test_read_into_rows_of_every_alignment(lrkv):
+    """fp32 rows 16 bytes past a 32-byte border, by pointer and by stride."""
+    cache, oc = _filled(lrkv, 1, 2, [150], "int8")
+    for shift, row in ((0, 128), (4, 128), (0, 132), (4, 136)):
+        buf = torch.full((2, 2 * 150 * row + 64), 2.0, device="cuda")
+        k, v = (x[shift:shift + 2 * 150 * row].view(1, 2, 150, row)[..., :128] for x in buf)
+        lrkv.quant_read(cache, k, v)
+        for h in range(2):
+            for side, x in enumerate((k, v)):
+                assert np.array_equal(x[0, h].cpu().numpy(), oc.values(0, h, side, np.float32))
+        assert int((buf == 2.0).sum()) >= 2 * (64 + 2 * 150 * (row - 128))
+
+
 def test_strided_inputs(lrkv):
     """k and v as slices of one fused projection [B, n, (H k, H v), 128]."""
     B, H, n = 2, 3, 77
