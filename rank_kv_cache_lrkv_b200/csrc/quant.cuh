@@ -154,6 +154,7 @@ int quant_append_launch(const QuantAppendArgs& a, cudaStream_t st);
 int quant_read_launch(const QuantReadArgs& a, int dtype, cudaStream_t st);
 size_t quant_attn_workspace(int B, int H, int Hq, int n);
 size_t quant_prefill_workspace(int C);
+int quant_few_launch(const QuantAttnArgs& a, const DevInfo& info, cudaStream_t st);
 int quant_prefill_launch(const QuantAttnArgs& a, const DevInfo& info, cudaStream_t st);
 int quant_attn_launch(const QuantAttnArgs& a, cudaStream_t st);
 

@@ -31,7 +31,7 @@ int check_quant_heads(const lrkv_quant_cache* c, int H_q, int n) {
   if (H_q / c->num_kv_heads > 128) return LRKV_ERR_UNSUPPORTED;
   // blocks of the whole batch and a unit's rows (queries x grouped heads) are
   // counted in 32 bits
-  if ((long long)c->batch * c->num_kv_heads * ((long long)c->max_pages_per_seq + 1) > INT_MAX)
+  if ((long long)c->batch * c->num_kv_heads * ((long long)c->max_pages_per_seq + 8) > INT_MAX)
     return LRKV_ERR_UNSUPPORTED;
   if ((long long)n * (H_q / c->num_kv_heads) > (1 << 30)) return LRKV_ERR_UNSUPPORTED;
   return LRKV_OK;

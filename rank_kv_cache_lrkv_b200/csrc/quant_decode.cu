@@ -728,7 +728,7 @@ size_t quant_attn_workspace(int, int H, int Hq, int n) {
   DevInfo info;
   if (current_device_info(dev, info) != LRKV_OK) return 0;
   // the counters come first in both layouts, the records need no zeros
-  return (long long)n * (Hq / H) <= kMaxRows ? dec_ws(info.sms) : quant_prefill_workspace(info.sms);
+  return (long long)n * (Hq / H) <= 8 ? dec_ws(info.sms) : quant_prefill_workspace(info.sms);
 }
 
 int quant_attn_launch(const QuantAttnArgs& a, cudaStream_t st) {
@@ -745,8 +745,7 @@ int quant_attn_launch(const QuantAttnArgs& a, cudaStream_t st) {
       return a.c.e4m3 ? launch<true, 1, 6, 2>(a, info, st) : launch<false, 1, 6, 2>(a, info, st);
     return a.c.e4m3 ? launch<true, 1, 5, 2>(a, info, st) : launch<false, 1, 5, 2>(a, info, st);
   }
-  if ((long long)a.n * a.G <= kMaxRows)
-    return a.c.e4m3 ? launch<true, 2, 4, 2>(a, info, st) : launch<false, 2, 4, 2>(a, info, st);
+  if ((long long)a.n * a.G <= 128) return quant_few_launch(a, info, st);
   return quant_prefill_launch(a, info, st);
 }
 

@@ -29,36 +29,22 @@
 // through records in the workspace, which a second launch folds in order.
 #include <type_traits>
 
-#include "quant.cuh"
-#include "tcgen05.cuh"
+#include "quant_tc.cuh"
 
 namespace lrkv {
 
 namespace {
 
-constexpr int kTileRows = 256;
-constexpr int kStepKeys = kQBlock;
 constexpr int kRing = 4;                        // key and value tiles in flight
 constexpr int kPreThreads = 512;
 constexpr int kQHalf = 128 * 128;               // 64 dims of a group's 128 rows of q
 constexpr int kQGroup = 2 * kQHalf;
-constexpr int kKHalf = kStepKeys * 128;         // 64 dims of a step's keys
-constexpr int kTileBytes = 2 * kKHalf;          // a step's keys, or its values [128][64]
 // A step's scales are read until its P is written; the converters are at most
 // kRing + 2 steps ahead of that.
 constexpr int kScaleRing = 8;
 // A tile's start and end (its rows of q and o, the empty pipeline) take about
 // as long as this many steps; the ranges count them.
 constexpr int kTileSteps = 4;
-constexpr float kLazy = 6.f;
-constexpr float kBoostLog = 8.f;
-
-struct StepScales {
-  float sk, sv;
-  int ok;       // the page's tokens count
-  int minbad;   // first open token whose value row is not finite
-};
-
 struct PrePlan {
   int q, k, v, bars, scales, parts, start, len, nq, sum, misc, total;
 };
@@ -80,106 +66,6 @@ __host__ __device__ inline PrePlan pre_plan(int B) {
   return p;
 }
 
-// Workspace: the counters of the few-row kernel (not used here, and left
-// alone), a cut per CTA (sequence, head, row and last CTA of the tile that
-// begins in it and goes on elsewhere; last CTA -1: none), two records per CTA
-// as in quant_decode.cu, of [33][256] float4: (m, l, M', -) of a row, then its
-// 128 sums four at a time, rows side by side.
-constexpr size_t kPreRecord = (size_t)33 * kTileRows;
-__host__ __device__ inline size_t pre_cuts(int C) { return ((size_t)C * 4 + 255) / 256 * 256; }
-__host__ __device__ inline size_t pre_records(int C) {
-  return pre_cuts(C) + ((size_t)C * 16 + 255) / 256 * 256;
-}
-
-// Shared-memory descriptors in halves: the upper one is the same for every
-// 128-byte-swizzled K-major tile, the lower one counts 16-byte units, so a
-// step within a tile is one addition (one thread issues all products).
-constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc,
-                                       uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
-      "r"(alo), "r"(blo), "r"(kDescHi), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t blo, uint32_t idesc,
-                                       uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "mov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "r"(blo), "r"(kDescHi), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// fp16 A and B, fp32 D, M = 128, both K-major; N = 64 keys or 128 dims.
-constexpr uint32_t kIdescS = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr uint32_t kIdescO = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(r));
-  return r != 0;
-}
-#define LRKV_R32(v, o)                                                                          \
-  "=r"(v[o + 0]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]),               \
-      "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7]), "=r"(v[o + 8]), "=r"(v[o + 9]),           \
-      "=r"(v[o + 10]), "=r"(v[o + 11]), "=r"(v[o + 12]), "=r"(v[o + 13]), "=r"(v[o + 14]),      \
-      "=r"(v[o + 15]), "=r"(v[o + 16]), "=r"(v[o + 17]), "=r"(v[o + 18]), "=r"(v[o + 19]),      \
-      "=r"(v[o + 20]), "=r"(v[o + 21]), "=r"(v[o + 22]), "=r"(v[o + 23]), "=r"(v[o + 24]),      \
-      "=r"(v[o + 25]), "=r"(v[o + 26]), "=r"(v[o + 27]), "=r"(v[o + 28]), "=r"(v[o + 29]),      \
-      "=r"(v[o + 30]), "=r"(v[o + 31])
-// 32 consecutive columns of this thread's lane, no wait.
-template <int kOff, int N>
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[N]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : LRKV_R32(v, kOff)
-      : "r"(addr));
-}
-// Wait for this thread's loads; ties 32 of their registers to the wait.
-template <int kOff, int N>
-__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[N]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[kOff + i]));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16};" ::"r"(addr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&v)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-template <int R>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // The line, in shared memory: per sequence its start, what one KV head takes
 // of it, its length and its queries.
 struct Line {
@@ -676,40 +562,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         vr[i] = slab ? __ldg(reinterpret_cast<const uint4*>(slab + kQSide + (32 * i + sub) * kQBlock + ch * 16))
                      : make_uint4(0, 0, 0, 0);
     };
-    // 16 codes -> 32 bytes of fp16 at chunks cc, cc + 1 of a swizzled row
-    auto put = [&](uint8_t* rowp, int row, int cc, const uint4& w) {
-      uint32_t h[8];
-      quant_half4<kE4M3>(w.x, h[0], h[1]);
-      quant_half4<kE4M3>(w.y, h[2], h[3]);
-      quant_half4<kE4M3>(w.z, h[4], h[5]);
-      quant_half4<kE4M3>(w.w, h[6], h[7]);
-      *reinterpret_cast<uint4*>(rowp + ((cc ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(rowp + (((cc + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-    };
-    // Largest finite |x| (bf16 bits) of the open block's nt rows of one side
-    // and the first row that is not all finite (64: none).  Every warp looks
-    // at all of them: no barrier among warps that a failed wait may part.
-    auto scan_open = [&](const __nv_bfloat16* rows, int nt, int& bad) {
-      uint32_t mx = 0;
-      int fb = 64;
-#pragma unroll 4
-      for (int i = 0; i < 32; ++i) {
-        const int t = 2 * i + (lane >> 4);
-        if (t < nt) {
-          const uint4 w = *(reinterpret_cast<const uint4*>(rows + t * kHeadDim) + (lane & 15));
-          const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int hl = 0; hl < 2; ++hl) {
-              const uint32_t x = (e[q] >> (16 * hl)) & 0x7fffu;
-              if (x < 0x7f80u) mx = max(mx, x); else fb = min(fb, t);
-            }
-        }
-      }
-      bad = (int)__reduce_min_sync(0xffffffffu, (uint32_t)fb);
-      return __reduce_max_sync(0xffffffffu, mx);
-    };
     bool live = true;
     PrePart p;
     if (lo < hi) p = find_part(line, lo, hi);
@@ -737,32 +589,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = 32 * (i >> 1) + sub;
-            put(kb + (i & 1) * kKHalf + row * 128, row, 2 * ch, kr[i]);
+            put_codes<kE4M3>(kb + (i & 1) * kKHalf + row * 128, row, 2 * ch, kr[i]);
           }
         }
         int minbad = 0x7fffffff;
         if (open) {
-          // keys of the open block: thread = (token, half of the dims)
-          const int tok = ct >> 1, side = ct & 1;
           const int nt = L - j * kQBlock;
           int bad;
-          int e = (int)(scan_open(quant_tail(c, p.b, p.h, 0, j * kQBlock), nt, bad) >> 7) - 127;
-          e = max(e, -100);
-          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-          sk = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
-          const uint4* src = reinterpret_cast<const uint4*>(quant_tail(c, p.b, p.h, 0, j * kQBlock + tok)) + 8 * side;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 w = tok < nt ? src[i] : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(kb + side * kKHalf + tok * 128 + ((i ^ (tok & 7)) << 4)) =
-                make_uint4(pack_h2(bf_lo(w.x) * up, bf_hi(w.x) * up),
-                           pack_h2(bf_lo(w.y) * up, bf_hi(w.y) * up),
-                           pack_h2(bf_lo(w.z) * up, bf_hi(w.z) * up),
-                           pack_h2(bf_lo(w.w) * up, bf_hi(w.w) * up));
-          }
-          const int ve = (int)(scan_open(quant_tail(c, p.b, p.h, 1, j * kQBlock), nt, bad) >> 7) - 127;
+          sk = open_keys(quant_tail(c, p.b, p.h, 0, j * kQBlock), nt, kb, ct);
+          sv = open_values_scale(quant_tail(c, p.b, p.h, 1, j * kQBlock), nt, ct, bad);
           if (bad < 64) minbad = j * kQBlock + bad;
-          sv = __uint_as_float((uint32_t)(127 - 7 + max(ve, -100)) << 23);
         }
         if (ct == 0) {
           StepScales* s = &scales[cnt % kScaleRing];
@@ -780,29 +616,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         if (cnt >= kRing && !quant_wait_warp(&vempty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
         if (!open) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) put(vb + (32 * i + sub) * 128, 32 * i + sub, 2 * ch, vr[i]);
+          for (int i = 0; i < 4; ++i)
+            put_codes<kE4M3>(vb + (32 * i + sub) * 128, 32 * i + sub, 2 * ch, vr[i]);
         } else {
-          // values of the open block: thread = dim
-          const __nv_bfloat16* vt = quant_tail(c, p.b, p.h, 1, j * kQBlock) + ct;
-          const int nt = L - j * kQBlock;
-          const float up = __uint_as_float((254u << 23) - __float_as_uint(sv));  // 1 / sv, a power of two
-#pragma unroll 1
-          for (int cc = 0; cc < 8; ++cc) {
-            uint32_t h[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float v[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int t = 8 * cc + 2 * q + e;
-                v[e] = t < nt ? __bfloat162float(vt[t * kHeadDim]) * up : 0.f;
-                if (!(fabsf(v[e]) < 1e30f)) v[e] = 0.f;  // reported by minbad
-              }
-              h[q] = pack_h2(v[0], v[1]);
-            }
-            *reinterpret_cast<uint4*>(vb + ct * 128 + ((cc ^ (ct & 7)) << 4)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
-          }
+          open_values(quant_tail(c, p.b, p.h, 1, j * kQBlock), L - j * kQBlock, vb, ct, sv);
         }
         fence_proxy_async_smem();
         mbar_arrive(&vfull[buf]);
@@ -950,6 +767,15 @@ __global__ void __launch_bounds__(256) quant_merge_kernel(QuantAttnArgs a, int C
 
 }  // namespace
 
+int quant_merge_launch(const QuantAttnArgs& a, int C, int rows, cudaStream_t st) {
+  QuantAttnArgs args = a;
+  void* p[] = {&args, &C};
+  return launch_pdl((const void*)quant_merge_kernel, dim3(C, (rows + 7) / 8), dim3(256), 0, st, p) ==
+                 cudaSuccess
+             ? LRKV_OK
+             : LRKV_ERR_CUDA;
+}
+
 size_t quant_prefill_workspace(int C) {
   return pre_records(C) + (size_t)C * 2 * kPreRecord * 16;
 }
@@ -966,12 +792,7 @@ int quant_prefill_launch(const QuantAttnArgs& a, const DevInfo& info, cudaStream
   void* p[] = {&args, &RT};
   if (launch_pdl(fn, dim3(info.sms), dim3(kPreThreads), smem, st, p) != cudaSuccess)
     return LRKV_ERR_CUDA;
-  int C = info.sms;
-  void* pm[] = {&args, &C};
-  return launch_pdl((const void*)quant_merge_kernel, dim3(C, kTileRows / 8), dim3(256), 0, st, pm) ==
-                 cudaSuccess
-             ? LRKV_OK
-             : LRKV_ERR_CUDA;
+  return quant_merge_launch(a, info.sms, kTileRows, st);
 }
 
 }  // namespace lrkv
