@@ -109,9 +109,10 @@ __device__ __forceinline__ bool quant_wait(uint64_t* bar, uint32_t parity, volat
     }
   }
 }
-// The same, taken by lane 0 for the whole warp.
+// The same for a whole warp: every lane looks once, lane 0 goes on waiting.
 __device__ __forceinline__ bool quant_wait_warp(uint64_t* bar, uint32_t parity, volatile int* fail,
                                                 int lane) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   int ok = 1;
   if (lane == 0) ok = quant_wait(bar, parity, fail) ? 1 : 0;
   return __shfl_sync(0xffffffffu, ok, 0) != 0;

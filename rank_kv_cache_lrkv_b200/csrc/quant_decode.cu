@@ -344,33 +344,36 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
             // ---- scores: sacc[s4][n]: tokens 16 (g / 2) + 4 s4 + g % 2 (+ 2)
             float sacc[4][NT][4];
 #pragma unroll
-            for (int s4 = 0; s4 < 4; ++s4) {
-              const int ta = 16 * (g >> 1) + 4 * s4 + (g & 1);
-              const uint8_t* ra = slab + ta * kHeadDim + ((t ^ ((g & 1) << 2)) << 4);
-              const uint8_t* rb = slab + ta * kHeadDim + ((t ^ 4 ^ ((g & 1) << 2)) << 4);
-              uint4 ka[2], kb[2];
-              ka[0] = *reinterpret_cast<const uint4*>(ra);
-              kb[0] = *reinterpret_cast<const uint4*>(ra + 2 * kHeadDim);
-              ka[1] = *reinterpret_cast<const uint4*>(rb);
-              kb[1] = *reinterpret_cast<const uint4*>(rb + 2 * kHeadDim);
+            for (int s4 = 0; s4 < 4; ++s4)
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sacc[s4][n][e] = 0.f;
+            // the four token groups side by side: their sums are chains of
+            // their own (one group after the other is one long chain)
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t wa[4] = {ka[hf].x, ka[hf].y, ka[hf].z, ka[hf].w};
-                const uint32_t wb[4] = {kb[hf].x, kb[hf].y, kb[hf].z, kb[hf].w};
+            for (int hf = 0; hf < 2; ++hf) {
+              uint4 ka[4], kb[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+              for (int s4 = 0; s4 < 4; ++s4) {
+                const uint8_t* rk = slab + (16 * (g >> 1) + 4 * s4 + (g & 1)) * kHeadDim +
+                                    ((t ^ (hf << 2) ^ ((g & 1) << 2)) << 4);
+                ka[s4] = *reinterpret_cast<const uint4*>(rk);
+                kb[s4] = *reinterpret_cast<const uint4*>(rk + 2 * kHeadDim);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int s4 = 0; s4 < 4; ++s4) {
+                  const uint32_t wa = k == 0 ? ka[s4].x : k == 1 ? ka[s4].y : k == 2 ? ka[s4].z : ka[s4].w;
+                  const uint32_t wb = k == 0 ? kb[s4].x : k == 1 ? kb[s4].y : k == 2 ? kb[s4].z : kb[s4].w;
                   uint32_t a0, a1, a2, a3;
-                  quant_half4<kE4M3>(wa[k], a0, a2);
-                  quant_half4<kE4M3>(wb[k], a1, a3);
+                  quant_half4<kE4M3>(wa, a0, a2);
+                  quant_half4<kE4M3>(wb, a1, a3);
 #pragma unroll
                   for (int n = 0; n < NT; ++n)
                     mma_f16(sacc[s4][n], a0, a1, a2, a3, qf[n][4 * hf + k][0], qf[n][4 * hf + k][1]);
                 }
-              }
             }
             // ---- softmax: one maximum per column and block
             const int base = i * kQBlock;
@@ -728,7 +731,7 @@ size_t quant_attn_workspace(int, int H, int Hq, int n) {
   DevInfo info;
   if (current_device_info(dev, info) != LRKV_OK) return 0;
   // the counters come first in both layouts, the records need no zeros
-  return (long long)n * (Hq / H) <= 8 ? dec_ws(info.sms) : quant_prefill_workspace(info.sms);
+  return (long long)n * (Hq / H) <= kMaxRows ? dec_ws(info.sms) : quant_prefill_workspace(info.sms);
 }
 
 int quant_attn_launch(const QuantAttnArgs& a, cudaStream_t st) {
@@ -745,6 +748,11 @@ int quant_attn_launch(const QuantAttnArgs& a, cudaStream_t st) {
       return a.c.e4m3 ? launch<true, 1, 6, 2>(a, info, st) : launch<false, 1, 6, 2>(a, info, st);
     return a.c.e4m3 ? launch<true, 1, 5, 2>(a, info, st) : launch<false, 1, 5, 2>(a, info, st);
   }
+  // Two row tiles hold twice the registers and combine twice the rows: seven
+  // warps of one slab (8 x 12000 tokens, 16 rows: 57.5 us; four of two 58.5,
+  // eight of one, which spills, 67.5; the tensor-memory kernel 97).
+  if ((long long)a.n * a.G <= kMaxRows)
+    return a.c.e4m3 ? launch<true, 2, 7, 1>(a, info, st) : launch<false, 2, 7, 1>(a, info, st);
   if ((long long)a.n * a.G <= 128) return quant_few_launch(a, info, st);
   return quant_prefill_launch(a, info, st);
 }

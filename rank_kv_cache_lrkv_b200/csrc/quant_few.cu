@@ -12,11 +12,13 @@
 // a copy's tokens (written once, at the start), so O of copy c is the sum over
 // its tokens; the copies and the two groups are added at the end of a unit.
 //
-// Persistent, one CTA per SM, 16 warps, the pages of all units dealt evenly:
-//  * warp 13: one bulk copy per page slab into a ring of NR (44 bytes a
+// Persistent, one CTA per SM, 18 warps, the pages of all units dealt evenly:
+//  * warp 17: one bulk copy per page slab into a ring of NR (44 bytes a
 //    nanosecond and SM from HBM want 60 KB and more in flight);
-//  * warps 8-11: converters, from the ring to fp16 tiles;
-//  * warp 12, one lane: Q K^T and P V;
+//  * warps 8-11 and 12-15: converters of keys and of values, from the ring to
+//    fp16 tiles (one set for both waited for P V before it turned to the next
+//    keys: 2900 clocks a page);
+//  * warp 16, one lane: Q K^T and P V;
 //  * warps 0-3 and 4-7: softmax of even and odd pages, S, P and O of their own.
 #include <type_traits>
 
@@ -26,16 +28,15 @@ namespace lrkv {
 
 namespace {
 
-constexpr int kFewThreads = 512;
-constexpr int kTiles = 2;        // fp16 tiles of keys, and of values, in flight
+constexpr int kFewThreads = 576;
+constexpr int kTiles = 3;        // fp16 tiles of keys, and of values, in flight
 constexpr int kFewScales = 8;    // a step's scales are read until its P is written
-constexpr int kCombPad = 36;     // floats of a row of 32 sums: no bank conflicts
 // What a unit's start and end take, in steps (as in quant_prefill.cu).
 constexpr int kUnitSteps = 6;
 constexpr uint32_t kTmemP = 128, kTmemO = 256;
 
 struct FewPlan {
-  int q, k, v, raw, comb, ml, rowst, fc, scales, bars, rawok, start, len, nq, misc, total;
+  int q, k, v, raw, ml, rowst, fc, scales, bars, rawok, start, len, nq, misc, total;
 };
 constexpr int kFewBars = 4 * kTiles + 2 * 8 + 2 + 9;
 __host__ __device__ inline FewPlan few_plan(int NR, int B) {
@@ -44,8 +45,7 @@ __host__ __device__ inline FewPlan few_plan(int NR, int B) {
   p.k = 128 * 256;
   p.v = p.k + kTiles * kTileBytes;
   p.raw = p.v + kTiles * kTileBytes;
-  p.comb = p.raw + NR * kQSlab;
-  p.ml = p.comb + 256 * kCombPad * 4;
+  p.ml = p.raw + NR * kQSlab;
   p.rowst = p.ml + 256 * 16;
   p.fc = p.rowst + 128 * 16;
   p.scales = p.fc + 128 * 4;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(&rawfull[i], 1);
-      mbar_init(&rawempty[i], 4);
+      mbar_init(&rawempty[i], 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 2);  // the products' commit and the issuer itself
@@ -127,13 +127,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
     mbar_init(mdone, 1);
     mbar_fence_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(taddr, 512);
     tmem_relinquish();
   }
   pdl_trigger();
   pdl_wait();
-  if (warp == 13) {
+  if (warp == 17) {
     const int per = (c.B + 31) / 32, b0 = min(c.B, lane * per), b1 = min(c.B, b0 + per);
     int own = 0;
 #pragma unroll 1
@@ -215,7 +215,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
     const uint32_t tP = tmem + lane_base + kTmemP + gr * 32, tO = tmem + lane_base + kTmemO + gr * 128;
     uint8_t* qs = sm + pl.q;
     float* fc = reinterpret_cast<float*>(sm + pl.fc);
-    float* comb = reinterpret_cast<float*>(sm + pl.comb);
+    // 32 sums of the 256 rows, in q's place (its products have ended by then),
+    // four at a time turned by the row: no bank conflicts
+    float4* comb = reinterpret_cast<float4*>(sm + pl.q);
     float4* ml = reinterpret_cast<float4*>(sm + pl.ml);
     float4* rowst = reinterpret_cast<float4*>(sm + pl.rowst);
     int4* cuts = reinterpret_cast<int4*>(static_cast<uint8_t*>(a.ws) + pre_cuts(gridDim.x));
@@ -414,10 +416,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
           tc_fence_before();
           mbar_arrive(&oempty[gr]);
         }
-        float* dst = comb + tid * kCombPad;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<float4*>(dst + 4 * e) =
+          comb[tid * 8 + (e ^ (tid & 7))] =
               make_float4(__uint_as_float(o[4 * e]) * mix, __uint_as_float(o[4 * e + 1]) * mix,
                           __uint_as_float(o[4 * e + 2]) * mix, __uint_as_float(o[4 * e + 3]) * mix);
         named_bar(1, 256);
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
           float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int i = 0; i < 2 * REP; ++i) {
-            const float4 u = *reinterpret_cast<const float4*>(comb + (i * kCopy + ro) * kCombPad + 4 * d4);
+            const float4 u = comb[(i * kCopy + ro) * 8 + (d4 ^ (ro & 7))];
             t.x += u.x;
             t.y += u.y;
             t.z += u.z;
@@ -452,54 +453,71 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
       if (!whole && tid == 0 && p.j0 == 0)
         cuts[blockIdx.x] = make_int4(p.b, p.h, 0, cta_of(p.first + p.steps - 1));
     }
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ================ converters
-    const int ct = tid - 256, sub = ct >> 2, ch = ct & 3;  // 32 rows x 4 chunks a round
-    uint32_t cnt = 0;                    // steps converted
-    int rs = 0;                          // ring stage and its phase
-    uint32_t rph = 0;
+    const bool keys = warp < 12;
+    const int ct = (tid - 256) & 127, sub = ct >> 2, ch = ct & 3;  // 32 rows x 4 chunks a round
+    uint64_t* tfull = keys ? kfull : vfull;
+    uint64_t* tempty = keys ? kempty : vempty;
+    uint32_t cnt = 0, tph = 1, rph = 0;  // steps converted; phases of the tiles and the ring
+    int buf = 0, rs = 0;
     bool live = true;
     for (int x = lo; x < hi && live; advance(p, x)) {
       const int L = slen[p.b];
       for (int j = p.j0; j < p.j1; ++j, ++cnt) {
-        const int buf = cnt % kTiles;
-        const uint32_t ph = (cnt / kTiles - 1) & 1;
-        uint8_t* kb = sm + pl.k + buf * kTileBytes;
-        uint8_t* vb = sm + pl.v + buf * kTileBytes;
         const bool full = (j + 1) * kQBlock <= L, open = !full && j * kQBlock < L;
         const uint8_t* raw = sm + pl.raw + rs * kQSlab;
+        uint8_t* tile = sm + (keys ? pl.k : pl.v) + buf * kTileBytes;
         bool there = false;
+        uint4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
         float sk = 1.f, sv = 1.f;
+        int minbad = 0x7fffffff;
         if (full) {
           if (!quant_wait_warp(&rawfull[rs], rph, fail, lane)) { live = false; break; }
-          there = rawok[rs] != 0;
+          there = rawok[rs] != 0;  // if not, zeros under weights of zero
           if (there) {
-            const float2 t = *reinterpret_cast<const float2*>(raw + 2 * kQSide);
-            sk = t.x;
-            sv = t.y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = *reinterpret_cast<const uint4*>(
+                  raw + (keys ? quant_k_chunk(32 * (i >> 1) + sub, ch + 4 * (i & 1))
+                              : kQSide + (32 * i + sub) * kQBlock + ch * 16));
+            if (keys && ct == 0) {
+              const float2 t = *reinterpret_cast<const float2*>(raw + 2 * kQSide);
+              sk = t.x;
+              sv = t.y;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&rawempty[rs]);  // the codes are in registers
+          if (++rs == NR) {
+            rs = 0;
+            rph ^= 1;
           }
         }
-        // absent pages: zeros under weights of zero
-        auto chunk = [&](int at) {
-          return there ? *reinterpret_cast<const uint4*>(raw + at) : make_uint4(0, 0, 0, 0);
-        };
-        if (cnt >= kTiles && !quant_wait_warp(&kempty[buf], ph, fail, lane)) { live = false; break; }
-        int minbad = 0x7fffffff;
+        if (!quant_wait_warp(&tempty[buf], tph, fail, lane)) { live = false; break; }
         if (open) {
           const int nt = L - j * kQBlock;
+          const __nv_bfloat16 *kt = quant_tail(c, p.b, p.h, 0, j * kQBlock),
+                              *vt = quant_tail(c, p.b, p.h, 1, j * kQBlock);
           int bad;
-          sk = open_keys(quant_tail(c, p.b, p.h, 0, j * kQBlock), nt, kb, ct);
-          sv = open_values_scale(quant_tail(c, p.b, p.h, 1, j * kQBlock), nt, ct, bad);
+          sv = open_values_scale(vt, nt, ct, bad);
           if (bad < 64) minbad = j * kQBlock + bad;
-        } else {
+          if (keys) sk = open_keys(kt, nt, tile, ct);
+          else open_values(vt, nt, tile, ct, sv);
+        } else if (keys) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = 32 * (i >> 1) + sub;
-            put_codes<kE4M3>(kb + (i & 1) * kKHalf + row * 128, row, 2 * ch,
-                             chunk(quant_k_chunk(row, ch + 4 * (i & 1))));
+            put_codes<kE4M3>(tile + (i & 1) * kKHalf + row * 128, row, 2 * ch, w[i]);
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            put_codes<kE4M3>(tile + (32 * i + sub) * 128, 32 * i + sub, 2 * ch, w[i]);
         }
-        if (ct == 0) {
+        if (keys && ct == 0) {
           StepScales* s = &scales[cnt % kFewScales];
           s->sk = sk;
           s->sv = sv;
@@ -507,29 +525,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
           s->minbad = minbad;
         }
         fence_proxy_async_smem();
-        mbar_arrive(&kfull[buf]);
-        if (cnt >= kTiles && !quant_wait_warp(&vempty[buf], ph, fail, lane)) { live = false; break; }
-        if (open) {
-          open_values(quant_tail(c, p.b, p.h, 1, j * kQBlock), L - j * kQBlock, vb, ct, sv);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            put_codes<kE4M3>(vb + (32 * i + sub) * 128, 32 * i + sub, 2 * ch,
-                             chunk(kQSide + (32 * i + sub) * kQBlock + ch * 16));
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&vfull[buf]);
-        if (full) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&rawempty[rs]);
-          if (++rs == NR) {
-            rs = 0;
-            rph ^= 1;
-          }
+        mbar_arrive(&tfull[buf]);
+        if (++buf == kTiles) {
+          buf = 0;
+          tph ^= 1;
         }
       }
     }
-  } else if (warp == 12) {
+  } else if (warp == 16) {
     // ================ products
     const uint32_t q0 = desc_lo(smem_u32(sm + pl.q)), k0 = desc_lo(smem_u32(sm + pl.k)),
                    v0 = desc_lo(smem_u32(sm + pl.v));
@@ -605,7 +608,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
       }
     }
     __syncwarp();
-  } else if (warp == 13) {
+  } else if (warp == 17) {
     // ================ loader
     const uint64_t pol = l2_evict_first_policy();
     int rs = 0, issued = 0;
@@ -655,7 +658,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 16) tmem_dealloc(tmem, 512);
   if (tid == 0 && *fail) quant_error(c, kErrTimeout);
 }
 
