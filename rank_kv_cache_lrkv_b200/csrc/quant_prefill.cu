@@ -48,7 +48,7 @@ constexpr int kTileSteps = 4;
 struct PrePlan {
   int q, k, v, bars, scales, parts, start, len, nq, sum, misc, total;
 };
-constexpr int kBars = 4 * kRing + 15;
+constexpr int kBars = 4 * kRing + 17;
 __host__ __device__ inline PrePlan pre_plan(int B) {
   PrePlan p;
   p.q = 0;
@@ -185,10 +185,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   const QuantView& c = a.c;
   const PrePlan pl = pre_plan(c.B);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + pl.bars);
-  // sfull, pfull: [group][S buffer]; odone: P V of the group's last step ended
+  // sfull, pfull: [group][S buffer]; odone: a step's P V ended, ofull: a part's
   uint64_t *kfull = bars, *kempty = kfull + kRing, *vfull = kempty + kRing, *vempty = vfull + kRing,
            *qfull = vempty + kRing, *sfull = qfull + 2, *pfull = sfull + 4, *odone = pfull + 4,
-           *oempty = odone + 2, *mdone = oempty + 2;
+           *ofull = odone + 2, *oempty = ofull + 2, *mdone = oempty + 2;
   StepScales* scales = reinterpret_cast<StepScales*>(sm + pl.scales);
   PrePart* parts = reinterpret_cast<PrePart*>(sm + pl.parts);  // [8]
   long long* start = reinterpret_cast<long long*>(sm + pl.start);
@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 128);
       mbar_init(&odone[i], 1);
+      mbar_init(&ofull[i], 1);
       mbar_init(&oempty[i], 128);
     }
     mbar_init(mdone, 1);
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     int4* cuts = reinterpret_cast<int4*>(static_cast<uint8_t*>(a.ws) + pre_cuts(gridDim.x));
     if (tid == 0) cuts[blockIdx.x] = make_int4(0, 0, 0, -1);
     uint32_t ns = 0;          // parity of the S tiles seen, a bit per buffer
-    uint32_t nd = 0;          // steps of this group in the parts before
+    uint32_t nd = 0, np = 0;  // steps of this group in the parts before, and such parts
     uint32_t done = 0;        // steps of the parts before
     // the part lives in shared memory: no registers for it in the loops below
     if (lo < hi) {
@@ -460,7 +461,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       float4* rec = records + ((size_t)2 * blockIdx.x + (p.j0 == 0 ? 1 : 0)) * kPreRecord + gr * 128 + row;
       const float fin = l == 0.f ? 0.f : ex2_approx(mv - m - kBoostLog) / l;
       if (n > 0) {
-        quant_wait_warp(&odone[gr], (nd + n - 1) & 1, fail, lane);
+        // (a barrier of its own: of odone's phases the last two may still be
+        // open here, and a wait by parity tells only one from the one before)
+        quant_wait_warp(&ofull[gr], np & 1, fail, lane);
+        ++np;
         nd += n;
         tc_fence_after();
       }
@@ -476,8 +480,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
         if (whole) {
-          // rows as bf16 where q's were (its products have ended), chunks of
-          // 16 bytes turned by the row
+          // rows as bf16 exactly where the same rows of q were (its products
+          // have ended): another warp may have its next q in place already
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t w[4];
@@ -486,7 +490,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
               w[k] = l == 0.f ? 0u
                               : pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * fin,
                                             __uint_as_float(o[8 * e + 2 * k + 1]) * fin);
-            *reinterpret_cast<uint4*>(qs + row * 256 + (((4 * q4 + e) ^ (row & 15)) << 4)) =
+            *reinterpret_cast<uint4*>(qs + (q4 >> 1) * kQHalf + row * 128 +
+                                      (((4 * (q4 & 1) + e) ^ (row & 7)) << 4)) =
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           const int rw = w0 + i + (lane >> 4);
           if (r < R)
             *reinterpret_cast<uint4*>(dst + (long long)hd * a.oh + (long long)tk * a.ot) =
-                *reinterpret_cast<const uint4*>(qs + rw * 256 + ((ch ^ (rw & 15)) << 4));
+                *reinterpret_cast<const uint4*>(qs + (ch >> 3) * kQHalf + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4));
           r += 2;
           for (hd += 2; hd >= a.G; hd -= a.G) ++tk;
         }
@@ -664,43 +669,61 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
               mma_ts(d, pa + 8 * kk, vb + ((kk * 32) >> 4), kIdescO, kk > 0 || i > 0 ? 1u : 0u);
             tc_commit(&odone[gr]);
           };
-          auto keys = [&](int i) {
-            return quant_wait(&kfull[(cnt + i) % kRing], ((cnt + i) / kRing) & 1, fail);
+          // A look at a barrier takes 200 clocks and more here (the tensor
+          // cores read shared memory most of the time), so each barrier is
+          // looked at before the products that precede its use are issued, and
+          // waited for only if it was not there yet.
+          // Tiles of step i: values follow keys, so both.
+          auto tiles = [&](int i, bool wait) {
+            uint64_t* bar = &vfull[(cnt + i) % kRing];
+            const uint32_t ph = ((cnt + i) / kRing) & 1;
+            return wait ? quant_wait(bar, ph, fail) : mbar_try_wait(bar, ph);
           };
           // P of the group's step i
-          auto weights = [&](int gr, int i, uint32_t np) {
-            return quant_wait(&pfull[2 * gr + (i & 1)], ((np >> (i & 1)) ^ (i >> 1)) & 1, fail);
+          auto weights = [&](int gr, int i, bool wait) {
+            uint64_t* bar = &pfull[2 * gr + (i & 1)];
+            const uint32_t ph = (((gr ? np1 : np0) >> (i & 1)) ^ (i >> 1)) & 1;
+            return wait ? quant_wait(bar, ph, fail) : mbar_try_wait(bar, ph);
           };
           if (n0 > 0) ok = quant_wait(&qfull[0], ns0 & 1, fail);
           if (ok && n1 > 0) ok = quant_wait(&qfull[1], ns1 & 1, fail);
           for (int i = 0; i < 2 && i < n && ok; ++i) {
-            ok = keys(i);
+            ok = quant_wait(&kfull[(cnt + i) % kRing], ((cnt + i) / kRing) & 1, fail);
             if (!ok) break;
             tc_fence_after();
             if (i < n0) scores(0, i);
             if (i < n1) scores(1, i);
             tc_commit(&kempty[(cnt + i) % kRing]);
           }
+          bool t_seen = false, w0_seen = false, w1_seen = false;
           for (int i = 0; i < n && ok; ++i) {
-            ok = quant_wait(&vfull[(cnt + i) % kRing], ((cnt + i) / kRing) & 1, fail);
-            if (ok && i + 2 < n) ok = keys(i + 2);
+            const int far = min(i + 2, n - 1);
+            if (!t_seen) ok = tiles(far, true);
             if (ok && i < n0) {
-              ok = weights(0, i, np0);
+              if (!w0_seen) ok = weights(0, i, true);
               // O's last sums have been read
               if (ok && i == 0 && ns0 > 0) ok = quant_wait(&oempty[0], (ns0 - 1) & 1, fail);
               if (!ok) break;
+              if (i < n1) w1_seen = weights(1, i, false);
               tc_fence_after();
               sums(0, i);
+              if (i == n0 - 1) tc_commit(&ofull[0]);
               if (i + 2 < n0) scores(0, i + 2);
             }
             if (ok && i < n1) {
-              ok = weights(1, i, np1);
+              if (!w1_seen) ok = weights(1, i, true);
               if (ok && i == 0 && ns1 > 0) ok = quant_wait(&oempty[1], (ns1 - 1) & 1, fail);
               if (!ok) break;
+              if (i + 1 < n0) w0_seen = weights(0, i + 1, false);
+              if (i + 1 < n) t_seen = tiles(min(i + 3, n - 1), false);
               tc_fence_after();
               sums(1, i);
+              if (i == n1 - 1) tc_commit(&ofull[1]);
               if (i + 2 < n1) scores(1, i + 2);
+            } else {
+              w0_seen = t_seen = false;
             }
+            w1_seen = false;
             tc_commit(&vempty[(cnt + i) % kRing]);
             if (i + 2 < n) tc_commit(&kempty[(cnt + i + 2) % kRing]);
           }

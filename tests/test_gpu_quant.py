@@ -464,6 +464,37 @@ def test_non_finite_queries(lrkv):
         assert not torch.isnan(o).any(-1)[0].cpu()[~want].any()
 
 
+@pytest.mark.parametrize("lens,G,n", [([4000, 3001], 4, 300), ([700, 64, 2500], 3, 260),
+                                      ([5000], 8, 16), ([3000, 129], 2, 40), ([9000, 10], 4, 4)])
+def test_long_calls_over_many_ranges(lrkv, lens, G, n):
+    """Units of many parts and CTAs of many units: every call, one after the
+    other, against the formula in 64 bits on the GPU."""
+    B, H = len(lens), 2
+    cache, _ = _filled(lrkv, B, H, lens, "int8")
+    L = max(lens)
+    k, v = (torch.zeros(B, H, L, 128, device="cuda") for _ in range(2))
+    lrkv.quant_read(cache, k, v)
+    q = _rows(4, B, H * G, n).cuda()
+    s = (q.double().view(B, H, G * n, 128) @ k.double().transpose(2, 3) * SCALE).view(B, H, G, n, L)
+    at = torch.tensor(lens, device="cuda")[:, None] - n + torch.arange(n, device="cuda")
+    seen = torch.arange(L, device="cuda") <= at[..., None]
+    p = torch.softmax(s.masked_fill(~seen[:, None, None], -1e300), -1) * seen.any(-1)[:, None, None, :, None]
+    ref = (p.view(B, H, G * n, L) @ v.double()).view(B, H * G, n, 128)
+    w = (p.view(B, H, G * n, L) @ v.double().abs()).view(B, H * G, n, 128)
+    # the bound above with ds <= 2^-10 (sum |q k| scale < 60 here) and its
+    # floors left out (no block is far from its neighbours)
+    tol = 2.0 ** -8 * ref.abs() + w * (2.0 ** -11 + 2 * L * 2.0 ** -24 + 2.0 ** -9)
+    ws = lrkv.quant_attn_workspace(cache, H * G, n)
+    first = None
+    for _ in range(6):
+        o = torch.zeros_like(q)
+        lrkv.quant_attn(cache, q, SCALE, o, ws)
+        assert bool(((o.double() - ref).abs() <= tol).all())
+        assert first is None or torch.equal(first, o)
+        first = o
+    assert cache.error() == 0
+
+
 @pytest.mark.parametrize("n", [1, 5, 100])
 def test_the_same_call_gives_the_same_bits(lrkv, n):
     cache, oc = _filled(lrkv, 3, 2, [900, 64, 2000], "int8")
