@@ -142,7 +142,14 @@ struct QuantAttnArgs {
   long long qs, qh, qt, os, oh, ot;
   float scale;
   void* ws;
+  uint32_t gmul, gshift;  // division by G (group_division)
 };
+// n / G for 0 <= n < 2^31: with s = ceil(log2 G), mul = floor(2^(31+s) / G) + 1
+// exceeds 2^(31+s) / G by at most 1, so n mul / 2^(31+s) exceeds n / G by at most
+// n / 2^(31+s) < 1 / G (Granlund and Montgomery, 1994).  mul 0: G is 1.
+__device__ __forceinline__ int div_group(const QuantAttnArgs& a, int n) {
+  return a.gmul ? (int)(__umulhi((uint32_t)n, a.gmul) >> a.gshift) : n;
+}
 
 // Queries of sequence b in this call.
 __device__ __forceinline__ int quant_queries(const QuantAttnArgs& a, int b) {

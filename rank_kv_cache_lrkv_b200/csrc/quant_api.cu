@@ -147,6 +147,10 @@ int lrkv_quant_attn(const lrkv_quant_cache* cache, const void* q, int32_t num_q_
   a.ot = o_token_stride;
   a.scale = scale;
   a.ws = workspace;
+  int s = 0;
+  while ((1 << s) < a.G) ++s;
+  a.gmul = a.G == 1 ? 0u : (uint32_t)((1ull << (31 + s)) / a.G + 1);
+  a.gshift = a.G == 1 ? 0u : (uint32_t)(s - 1);
   return quant_attn_launch(a, static_cast<cudaStream_t>(stream));
 }
 

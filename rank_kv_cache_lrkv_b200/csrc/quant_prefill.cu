@@ -44,7 +44,7 @@ constexpr int kQGroup = 2 * kQHalf;
 constexpr int kScaleRing = 8;
 // A tile's start and end (its rows of q and o, the empty pipeline) take about
 // as long as this many steps; the ranges count them.
-constexpr int kTileSteps = 4;
+constexpr int kTileSteps = 8;
 struct PrePlan {
   int q, k, v, bars, scales, parts, start, len, nq, sum, misc, total;
 };
@@ -72,12 +72,13 @@ struct Line {
   const long long* start;
   const int *sum, *len, *nq;
   int B, G;
+  const QuantAttnArgs* a;
 };
 // Steps that group gr of row tile rt of sequence b needs.
 __device__ __forceinline__ int group_steps(const Line& n, int b, int rt, int gr) {
   const int R = n.nq[b] * n.G, r = rt * kTileRows + gr * 128;
   if (r >= R) return 0;
-  const int maxpos = n.len[b] - n.nq[b] + min(R - 1, r + 127) / n.G;
+  const int maxpos = n.len[b] - n.nq[b] + div_group(*n.a, min(R - 1, r + 127));
   return maxpos < 0 ? 0 : maxpos / kStepKeys + 1;
 }
 // Steps of a tile (its last group with rows needs most): one at least for
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     tmem_relinquish();
   }
   __syncthreads();
-  const Line line = {start, ssum, slen, snq, c.B, a.G};
+  const Line line = {start, ssum, slen, snq, c.B, a.G, &a};
   // a warp per sequence: the steps of its tiles
 #pragma unroll 1
   for (int b = warp; b < c.B; b += kPreThreads / 32) {
@@ -303,8 +304,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         const int nq = snq[p.b], pos0 = slen[p.b] - nq;
         const int rr = p.r0 + gr * 128 + row;
         const bool valid = rr < nq * a.G;
-        const int pos = valid ? pos0 + rr / a.G : 0x7fffffff;
-        const int minpos = pos0 + (p.r0 + gr * 128) / a.G;
+        const int pos = valid ? pos0 + div_group(a, rr) : 0x7fffffff;
+        const int minpos = pos0 + div_group(a, p.r0 + gr * 128);
         n = min(p.j1, p.ntile(gr)) - p.j0;
         const uint32_t steps = max(0, min(p.j1, max(p.nt0, p.nt1)) - p.j0);
         if (n > 0) {
@@ -316,15 +317,30 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         {
           const int w0 = row & ~31, R = nq * a.G, ch = lane & 15;
           int r = p.r0 + gr * 128 + w0 + (lane >> 4);
-          int tk = r / a.G, hd = r - tk * a.G;
-          const __nv_bfloat16* src = a.q + p.b * a.qs + (long long)(p.h * a.G) * a.qh + 8 * ch;
-#pragma unroll 4
+          const int tk = div_group(a, r);
+          int hd = r - tk * a.G;
+          const __nv_bfloat16* src = a.q + p.b * a.qs + (long long)(p.h * a.G + hd) * a.qh +
+                                     (long long)tk * a.qt + 8 * ch;
+          const long long two = 2 * a.qh, wrap = a.qt - a.G * a.qh;
+          const uint32_t to = smem_u32(qs + (ch >> 3) * kQHalf + (w0 + (lane >> 4)) * 128);
+#pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const int rw = w0 + i + (lane >> 4);
-            cp_async16(qs + (ch >> 3) * kQHalf + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4),
-                       r < R ? src + (long long)hd * a.qh + (long long)tk * a.qt : a.q, r < R ? 16 : 0);
+            const int rw = i + (lane >> 4);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             to + i * 128 + (((ch & 7) ^ (rw & 7)) << 4)),
+                         "l"(r < R ? src : a.q), "r"(r < R ? 16 : 0)
+                         : "memory");
             r += 2;
-            for (hd += 2; hd >= a.G; hd -= a.G) ++tk;
+            src += two;
+            hd += 2;
+            if (hd >= a.G) {
+              hd -= a.G;
+              src += wrap;
+            }
+            if (hd >= a.G) {  // G is 1
+              hd -= a.G;
+              src += wrap;
+            }
           }
           cp_async_commit();
           cp_async_wait<0>();
@@ -468,8 +484,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         nd += n;
         tc_fence_after();
       }
-      // (unrolled once: O's registers are the loop's)
-#pragma unroll 1
+#pragma unroll 2
       for (int q4 = 0; q4 < 4; ++q4) {
         uint32_t o[32];
         if (n > 0) {
@@ -511,16 +526,29 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         // two whole rows of the warp's 32 at a time
         const int w0 = row & ~31, R = snq[p.b] * a.G, ch = lane & 15;
         int r = p.r0 + gr * 128 + w0 + (lane >> 4);
-        int tk = r / a.G, hd = r - tk * a.G;
-        __nv_bfloat16* dst = a.o + p.b * a.os + (long long)(p.h * a.G) * a.oh + 8 * ch;
-#pragma unroll 4
+        const int tk = div_group(a, r);
+        int hd = r - tk * a.G;
+        __nv_bfloat16* dst = a.o + p.b * a.os + (long long)(p.h * a.G + hd) * a.oh +
+                             (long long)tk * a.ot + 8 * ch;
+        const long long two = 2 * a.oh, wrap = a.ot - a.G * a.oh;
+        const uint8_t* from = qs + (ch >> 3) * kQHalf + (w0 + (lane >> 4)) * 128;
+#pragma unroll 8
         for (int i = 0; i < 32; i += 2) {
-          const int rw = w0 + i + (lane >> 4);
+          const int rw = i + (lane >> 4);
           if (r < R)
-            *reinterpret_cast<uint4*>(dst + (long long)hd * a.oh + (long long)tk * a.ot) =
-                *reinterpret_cast<const uint4*>(qs + (ch >> 3) * kQHalf + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4));
+            *reinterpret_cast<uint4*>(dst) =
+                *reinterpret_cast<const uint4*>(from + i * 128 + (((ch & 7) ^ (rw & 7)) << 4));
           r += 2;
-          for (hd += 2; hd >= a.G; hd -= a.G) ++tk;
+          dst += two;
+          hd += 2;
+          if (hd >= a.G) {
+            hd -= a.G;
+            dst += wrap;
+          }
+          if (hd >= a.G) {  // G is 1
+            hd -= a.G;
+            dst += wrap;
+          }
         }
       }
       if (!whole) {
