@@ -16,8 +16,10 @@
 //    bytes to two fp16 numbers, into the 128-byte-swizzled K-major tiles
 //    (keys as rows for Q K^T; the stored transpose of V is already K-major
 //    for P V).  The open block's bf16 rows become fp16 under a power of two.
-//  * warp 12, one lane: per step and group P V (A from TMEM), then Q K^T of
-//    the step after the next into the S that P has just left.
+//  * warps 12 and 13, one lane each, for group 0 and 1: per step P V (A from
+//    TMEM), then Q K^T of the step after the next into the S that P has just
+//    left.  (One thread for both needed 2000 clocks a step to issue what takes
+//    the tensor cores 1240.)
 // A row keeps its references m (scores) and M' (scores + floor(log2 s_v)) as
 // long as they lag by at most 2^kLazy, so O is seldom rescaled; a weight is
 // then at most 2^(1 + kLazy + kBoostLog) = 2^15 and fp16's floor lies 2^-33
@@ -204,9 +206,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     *fail = 0;
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&kfull[i], 128);
-      mbar_init(&kempty[i], 1);
+      mbar_init(&kempty[i], 2);  // both groups' issuers
       mbar_init(&vfull[i], 128);
-      mbar_init(&vempty[i], 1);
+      mbar_init(&vempty[i], 2);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sfull[i], 2);  // the products' commit and the issuer itself
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       mbar_init(&ofull[i], 1);
       mbar_init(&oempty[i], 128);
     }
-    mbar_init(mdone, 1);
+    mbar_init(mdone, 2);
     mbar_fence_init();
   }
   pdl_trigger();
@@ -662,26 +664,25 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   } else {
     // ================ products
     regs_dec<80>();
-    if (warp == 12) {
-      const uint32_t q0 = desc_lo(smem_u32(sm + pl.q)), k0 = desc_lo(smem_u32(sm + pl.k)),
-                     v0 = desc_lo(smem_u32(sm + pl.v));
-      // steps; per group the parity of its P tiles, a bit per buffer, and its
-      // parts
-      uint32_t cnt = 0, np0 = 0, np1 = 0, ns0 = 0, ns1 = 0;
+    if (warp < 14) {
+      const int gr = warp - 12;
+      const uint32_t qa = desc_lo(smem_u32(sm + pl.q)) + gr * (kQGroup >> 4),
+                     k0 = desc_lo(smem_u32(sm + pl.k)), v0 = desc_lo(smem_u32(sm + pl.v)),
+                     dS = tmem + gr * 128, dO = tmem + 256 + gr * 128;
+      // steps of the tiles; parity of this group's P, a bit per buffer; its parts
+      uint32_t cnt = 0, np = 0, ns = 0;
       bool live = true;
       PrePart p;
       if (lo < hi) p = find_part(line, lo, hi);
       for (long long x = lo; x < hi && live; advance(p, x)) {
         const int j1 = min(p.j1, max(p.nt0, p.nt1)), n = max(0, j1 - p.j0);
-        // the groups' steps here
-        const int n0 = max(0, min(p.j1, p.nt0) - p.j0), n1 = max(0, min(p.j1, p.nt1) - p.j0);
+        const int mine = max(0, min(p.j1, p.ntile(gr)) - p.j0);  // this group's steps
         bool ok = true;
         if (n > 0 && elect_one()) {
-          // S of group gr, step i; the issuer's own arrival hands on what it
-          // has seen of the converters (the scales)
-          auto scores = [&](int gr, int i) {
-            const uint32_t d = tmem + gr * 128 + (i & 1) * 64, qa = q0 + gr * (kQGroup >> 4),
-                           kb = k0 + ((cnt + i) % kRing) * (kTileBytes >> 4);
+          // S of step i; the issuer's own arrival hands on what it has seen of
+          // the converters (the scales)
+          auto scores = [&](int i) {
+            const uint32_t d = dS + (i & 1) * 64, kb = k0 + ((cnt + i) % kRing) * (kTileBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               mma_ss(d, qa + (((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4),
@@ -689,77 +690,59 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
             tc_commit(&sfull[2 * gr + (i & 1)]);
             mbar_arrive(&sfull[2 * gr + (i & 1)]);
           };
-          auto sums = [&](int gr, int i) {
-            const uint32_t d = tmem + 256 + gr * 128, pa = tmem + gr * 128 + (i & 1) * 64,
-                           vb = v0 + ((cnt + i) % kRing) * (kTileBytes >> 4);
+          auto sums = [&](int i) {
+            const uint32_t pa = dS + (i & 1) * 64, vb = v0 + ((cnt + i) % kRing) * (kTileBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_ts(d, pa + 8 * kk, vb + ((kk * 32) >> 4), kIdescO, kk > 0 || i > 0 ? 1u : 0u);
+              mma_ts(dO, pa + 8 * kk, vb + ((kk * 32) >> 4), kIdescO, kk > 0 || i > 0 ? 1u : 0u);
             tc_commit(&odone[gr]);
           };
           // A look at a barrier takes 200 clocks and more here (the tensor
-          // cores read shared memory most of the time), so each barrier is
-          // looked at before the products that precede its use are issued, and
-          // waited for only if it was not there yet.
-          // Tiles of step i: values follow keys, so both.
+          // cores read shared memory most of the time), so the next step's
+          // tiles (values follow keys, so both) are looked at before this
+          // step's products are issued, and waited for only if they were not
+          // there yet.
           auto tiles = [&](int i, bool wait) {
             uint64_t* bar = &vfull[(cnt + i) % kRing];
             const uint32_t ph = ((cnt + i) / kRing) & 1;
             return wait ? quant_wait(bar, ph, fail) : mbar_try_wait(bar, ph);
           };
-          // P of the group's step i
-          auto weights = [&](int gr, int i, bool wait) {
-            uint64_t* bar = &pfull[2 * gr + (i & 1)];
-            const uint32_t ph = (((gr ? np1 : np0) >> (i & 1)) ^ (i >> 1)) & 1;
-            return wait ? quant_wait(bar, ph, fail) : mbar_try_wait(bar, ph);
-          };
-          if (n0 > 0) ok = quant_wait(&qfull[0], ns0 & 1, fail);
-          if (ok && n1 > 0) ok = quant_wait(&qfull[1], ns1 & 1, fail);
+          if (mine > 0) ok = quant_wait(&qfull[gr], ns & 1, fail);
           for (int i = 0; i < 2 && i < n && ok; ++i) {
             ok = quant_wait(&kfull[(cnt + i) % kRing], ((cnt + i) / kRing) & 1, fail);
             if (!ok) break;
             tc_fence_after();
-            if (i < n0) scores(0, i);
-            if (i < n1) scores(1, i);
+            if (i < mine) scores(i);
             tc_commit(&kempty[(cnt + i) % kRing]);
           }
-          bool t_seen = false, w0_seen = false, w1_seen = false;
+          bool seen = false;
           for (int i = 0; i < n && ok; ++i) {
-            const int far = min(i + 2, n - 1);
-            if (!t_seen) ok = tiles(far, true);
-            if (ok && i < n0) {
-              if (!w0_seen) ok = weights(0, i, true);
+            // an issuer whose group has ended keeps pace with the tiles: each
+            // is given back by both, once
+            if (!seen) ok = tiles(min(i + 2, n - 1), true);
+            if (ok && i < mine) {
+              ok = quant_wait(&pfull[2 * gr + (i & 1)], ((np >> (i & 1)) ^ (i >> 1)) & 1, fail);
               // O's last sums have been read
-              if (ok && i == 0 && ns0 > 0) ok = quant_wait(&oempty[0], (ns0 - 1) & 1, fail);
-              if (!ok) break;
-              if (i < n1) w1_seen = weights(1, i, false);
-              tc_fence_after();
-              sums(0, i);
-              if (i == n0 - 1) tc_commit(&ofull[0]);
-              if (i + 2 < n0) scores(0, i + 2);
+              if (ok && i == 0 && ns > 0) ok = quant_wait(&oempty[gr], (ns - 1) & 1, fail);
             }
-            if (ok && i < n1) {
-              if (!w1_seen) ok = weights(1, i, true);
-              if (ok && i == 0 && ns1 > 0) ok = quant_wait(&oempty[1], (ns1 - 1) & 1, fail);
-              if (!ok) break;
-              if (i + 1 < n0) w0_seen = weights(0, i + 1, false);
-              if (i + 1 < n) t_seen = tiles(min(i + 3, n - 1), false);
+            if (!ok) break;
+            seen = i + 1 < n && tiles(min(i + 3, n - 1), false);
+            if (i < mine) {
               tc_fence_after();
-              sums(1, i);
-              if (i == n1 - 1) tc_commit(&ofull[1]);
-              if (i + 2 < n1) scores(1, i + 2);
-            } else {
-              w0_seen = t_seen = false;
+              sums(i);
+              if (i == mine - 1) tc_commit(&ofull[gr]);
+              if (i + 2 < mine) scores(i + 2);
             }
-            w1_seen = false;
             tc_commit(&vempty[(cnt + i) % kRing]);
             if (i + 2 < n) tc_commit(&kempty[(cnt + i + 2) % kRing]);
           }
         }
         live = __all_sync(0xffffffffu, ok);
         cnt += n;
-        if (n0 > 0) { np0 ^= (((n0 + 1) >> 1) & 1) | (((n0 >> 1) & 1) << 1); ++ns0; }
-        if (n1 > 0) { np1 ^= (((n1 + 1) >> 1) & 1) | (((n1 >> 1) & 1) << 1); ++ns1; }
+        if (mine > 0) {
+          np ^= (((mine + 1) >> 1) & 1) | (((mine >> 1) & 1) << 1);
+          ++ns;
+        }
       }
       // every product has ended before TMEM is freed
       if (works && elect_one()) {
