@@ -36,6 +36,10 @@ __device__ __forceinline__ uint8_t* quant_slab(const QuantView& c, int b, int h,
   if (page < 0 || page >= c.num_pages) return nullptr;
   return c.pages + ((size_t)page * c.H + h) * kQSlab;
 }
+// Brings bytes (a multiple of 16, from a 16-byte boundary) into L2.
+__device__ __forceinline__ void l2_prefetch(const void* p, int bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 // Row of token t in the tail (side 0: keys, 1: values).
 __device__ __forceinline__ __nv_bfloat16* quant_tail(const QuantView& c, int b, int h, int side,
                                                      int t) {

@@ -44,6 +44,7 @@ constexpr int kQGroup = 2 * kQHalf;
 // A step's scales are read until its P is written; the converters are at most
 // kRing + 2 steps ahead of that.
 constexpr int kScaleRing = 8;
+constexpr int kFar = 3;                         // steps ahead at which a page is brought into L2
 // A tile's start and end (its rows of q and o, the empty pipeline) take about
 // as long as this many steps; the ranges count them.
 constexpr int kTileSteps = 8;
@@ -574,12 +575,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     uint32_t cnt = 0;     // steps converted
     const uint8_t* slab;  // slab of a step (nullptr: open, or out of range)
     float2 nsc;           // its scales
-    auto page = [&](const PrePart& p, int j) {
+    int next = 0, far = 0;  // table entries of the steps j + 1 and j + kFar
+    auto entry = [&](const PrePart& p, int j) {
+      return (j + 1) * kQBlock <= slen[p.b] ? c.bt[(size_t)p.b * c.maxp + j] : -1;
+    };
+    auto page = [&](const PrePart& p, int j, int id) {
       slab = nullptr;
       if ((j + 1) * kQBlock <= slen[p.b]) {
-        slab = quant_slab(c, p.b, p.h, j);
-        if (slab) nsc = __ldg(reinterpret_cast<const float2*>(slab + 2 * kQSide));
-        else if (ct == 0) quant_error(c, kErrBadPage);
+        if (id >= 0 && id < c.num_pages) {
+          slab = c.pages + ((size_t)id * c.H + p.h) * kQSlab;
+          nsc = __ldg(reinterpret_cast<const float2*>(slab + 2 * kQSide));
+        } else if (ct == 0) {
+          quant_error(c, kErrBadPage);
+        }
       }
     };
     // keys: token 32 (i / 2) + sub, chunk ch + 4 (i % 2); a quarter warp then
@@ -604,8 +612,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       const int L = slen[p.b], last = max(p.nt0, p.nt1);
       const int j1 = min(p.j1, last);
       if (p.j0 < j1) {
-        page(p, p.j0);
+        page(p, p.j0, entry(p, p.j0));
         load_k();
+        next = entry(p, p.j0 + 1);
+        far = entry(p, p.j0 + kFar);
       }
       for (int j = p.j0; j < j1; ++j) {
         const int buf = cnt % kRing;
@@ -645,8 +655,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         fence_proxy_async_smem();
         mbar_arrive(&kfull[buf]);
         if (j + 1 < j1) {
-          page(p, j + 1);
+          page(p, j + 1, next);
           load_k();
+          next = entry(p, j + 2);
+          if (ct == 0) {
+            if (j + kFar < j1 && far >= 0 && far < c.num_pages)
+              l2_prefetch(c.pages + ((size_t)far * c.H + p.h) * kQSlab, kQSlab);
+            far = entry(p, j + 1 + kFar);
+          }
         }
         if (cnt >= kRing && !quant_wait_warp(&vempty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
         if (!open) {
@@ -698,14 +714,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
             tc_commit(&odone[gr]);
           };
           // A look at a barrier takes 200 clocks and more here (the tensor
-          // cores read shared memory most of the time), so the next step's
-          // tiles (values follow keys, so both) are looked at before this
-          // step's products are issued, and waited for only if they were not
-          // there yet.
+          // cores read shared memory most of the time), so the tiles of the
+          // next step's products (V of step i, K of step i + 2) are looked at
+          // before this step's products are issued, and waited for only if
+          // they were not there yet.
           auto tiles = [&](int i, bool wait) {
-            uint64_t* bar = &vfull[(cnt + i) % kRing];
-            const uint32_t ph = ((cnt + i) / kRing) & 1;
-            return wait ? quant_wait(bar, ph, fail) : mbar_try_wait(bar, ph);
+            auto look = [&](uint64_t* bars, int k) {
+              uint64_t* bar = &bars[(cnt + k) % kRing];
+              const uint32_t ph = ((cnt + k) / kRing) & 1;
+              return wait ? quant_wait(bar, ph, fail) : mbar_try_wait(bar, ph);
+            };
+            const bool v = look(vfull, i);
+            return (i + 2 < n ? look(kfull, i + 2) : true) && v;
           };
           if (mine > 0) ok = quant_wait(&qfull[gr], ns & 1, fail);
           for (int i = 0; i < 2 && i < n && ok; ++i) {
@@ -719,14 +739,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           for (int i = 0; i < n && ok; ++i) {
             // an issuer whose group has ended keeps pace with the tiles: each
             // is given back by both, once
-            if (!seen) ok = tiles(min(i + 2, n - 1), true);
+            if (!seen) ok = tiles(i, true);
             if (ok && i < mine) {
               ok = quant_wait(&pfull[2 * gr + (i & 1)], ((np >> (i & 1)) ^ (i >> 1)) & 1, fail);
               // O's last sums have been read
               if (ok && i == 0 && ns > 0) ok = quant_wait(&oempty[gr], (ns - 1) & 1, fail);
             }
             if (!ok) break;
-            seen = i + 1 < n && tiles(min(i + 3, n - 1), false);
+            seen = i + 1 < n && tiles(i + 1, false);
             if (i < mine) {
               tc_fence_after();
               sums(i);
