@@ -49,7 +49,7 @@ constexpr int kFar = 3;                         // steps ahead at which a page i
 // as long as this many steps; the ranges count them.
 constexpr int kTileSteps = 8;
 struct PrePlan {
-  int q, k, v, bars, scales, parts, start, len, nq, sum, misc, total;
+  int q, k, v, bars, scales, parts, misc, start, len, nq, sum, total;
 };
 constexpr int kBars = 4 * kRing + 17;
 __host__ __device__ inline PrePlan pre_plan(int B) {
@@ -60,12 +60,12 @@ __host__ __device__ inline PrePlan pre_plan(int B) {
   p.bars = p.v + kRing * kTileBytes;
   p.scales = (p.bars + kBars * 8 + 15) / 16 * 16;
   p.parts = p.scales + kScaleRing * (int)sizeof(StepScales);
-  p.start = p.parts + 8 * 48;
+  p.misc = p.parts + 8 * 48;
+  p.start = p.misc + 64;
   p.sum = p.start + (B + 1) * 8;
   p.len = p.sum + B * 4;
   p.nq = p.len + B * 4;
-  p.misc = p.nq + B * 4;
-  p.total = (p.misc + 64 + 15) / 16 * 16;
+  p.total = (p.nq + B * 4 + 15) / 16 * 16;
   return p;
 }
 
@@ -181,6 +181,12 @@ __device__ __forceinline__ PrePart next_part(const Line& n, const PrePart& p, lo
   return q;
 }
 
+// The CTA whose range holds the place before x.
+__device__ __forceinline__ int last_cta(const Line& n, long long x) {
+  const long long total = *static_cast<const volatile long long*>(&n.start[n.B]);
+  return (int)((x * min((long long)gridDim.x, total) - 1) / total);
+}
+
 template <bool kE4M3>
 __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttnArgs a, int RT) {
   extern __shared__ __align__(1024) uint8_t sm_raw[];
@@ -269,11 +275,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *taddr;
-  const long long total = start[c.B];
-  const int C = (int)min((long long)gridDim.x, total);
-  const bool works = (int)blockIdx.x < C;
-  const long long lo = works ? total * blockIdx.x / C : 0;
-  const long long hi = works ? total * (blockIdx.x + 1) / C : 0;
+  long long lo = 0, hi = 0;
+  {
+    const long long total = start[c.B];
+    const int C = (int)min((long long)gridDim.x, total);
+    if ((int)blockIdx.x < C) {
+      lo = total * blockIdx.x / C;
+      hi = total * (blockIdx.x + 1) / C;
+    }
+  }
 
   // the parts of this range, one after the other: `x` is where the part begins
   auto advance = [&](PrePart& p, long long& x) {
@@ -283,7 +293,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
 
   if (warp < 8) {
     // ================ softmax
-    regs_inc<152>();  // of 4 x 128 registers: 152 + 152 + 128 + 80
     const int gr = warp >> 2, row = tid & 127;  // TMEM lane = row of the group
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + gr * 128, tO = tmem + lane_base + 256 + gr * 128;
@@ -306,8 +315,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         const PrePart p = parts[warp];
         const int nq = snq[p.b], pos0 = slen[p.b] - nq;
         const int rr = p.r0 + gr * 128 + row;
-        const bool valid = rr < nq * a.G;
-        const int pos = valid ? pos0 + div_group(a, rr) : 0x7fffffff;
+        const int pos = rr < nq * a.G ? pos0 + div_group(a, rr) : 0x7fffffff;
         const int minpos = pos0 + div_group(a, p.r0 + gr * 128);
         n = min(p.j1, p.ntile(gr)) - p.j0;
         const uint32_t steps = max(0, min(p.j1, max(p.nt0, p.nt1)) - p.j0);
@@ -463,7 +471,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           };
           if (edge) weigh(std::true_type()); else weigh(std::false_type());
           l += sum.x + sum.y;
-          if (sc.minbad <= pos && valid) l = NAN;  // a value row that is not finite is seen
+          // a value row that is not finite is seen (in rows that are not
+          // there, always: nobody reads them)
+          if (sc.minbad <= pos) l = NAN;
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&pfull[2 * gr + sb]);
@@ -558,8 +568,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         rec[0] = st;
         // a tile that begins in this CTA and goes on in others: for the merge
         if (tid == 0 && p.j0 == 0)
-          cuts[blockIdx.x] = make_int4(p.b, p.h, p.r0,
-                                       (int)(((p.first + p.steps) * C - 1) / total));
+          cuts[blockIdx.x] = make_int4(p.b, p.h, p.r0, last_cta(line, p.first + p.steps));
       }
       }
       advance(p, x);
@@ -679,7 +688,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     }
   } else {
     // ================ products
-    regs_dec<80>();
     if (warp < 14) {
       const int gr = warp - 12;
       const uint32_t qa = desc_lo(smem_u32(sm + pl.q)) + gr * (kQGroup >> 4),
@@ -765,7 +773,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         }
       }
       // every product has ended before TMEM is freed
-      if (works && elect_one()) {
+      if (lo < hi && elect_one()) {
         tc_commit(mdone);
         const uint64_t t0 = global_ns();
         while (!mbar_try_wait(mdone, 0) && global_ns() - t0 < kTcTimeoutNs) {
@@ -777,7 +785,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 12) tmem_dealloc(*static_cast<volatile uint32_t*>(taddr), 512);
   if (tid == 0 && *fail) quant_error(c, kErrTimeout);
 }
 
