@@ -36,7 +36,7 @@ constexpr int kUnitSteps = 6;
 constexpr uint32_t kTmemP = 128, kTmemO = 256;
 
 struct FewPlan {
-  int q, k, v, raw, ml, rowst, fc, scales, bars, rawok, start, len, nq, misc, total;
+  int q, k, v, ml, rowst, fc, scales, bars, rawok, misc, raw, start, len, nq, total;
 };
 constexpr int kFewBars = 4 * kTiles + 2 * 8 + 2 + 9;
 __host__ __device__ inline FewPlan few_plan(int NR, int B) {
@@ -44,18 +44,18 @@ __host__ __device__ inline FewPlan few_plan(int NR, int B) {
   p.q = 0;
   p.k = 128 * 256;
   p.v = p.k + kTiles * kTileBytes;
-  p.raw = p.v + kTiles * kTileBytes;
-  p.ml = p.raw + NR * kQSlab;
+  p.ml = p.v + kTiles * kTileBytes;
   p.rowst = p.ml + 256 * 16;
   p.fc = p.rowst + 128 * 16;
   p.scales = p.fc + 128 * 4;
   p.bars = p.scales + kFewScales * (int)sizeof(StepScales);
   p.rawok = p.bars + kFewBars * 8;
-  p.start = p.rawok + 8 * 4;
+  p.misc = p.rawok + 8 * 4;
+  p.raw = (p.misc + 16 + 127) / 128 * 128;
+  p.start = p.raw + NR * kQSlab;
   p.len = p.start + (B + 1) * 4;
   p.nq = p.len + B * 4;
-  p.misc = p.nq + B * 4;
-  p.total = p.misc + 16;
+  p.total = p.nq + B * 4;
   return p;
 }
 
