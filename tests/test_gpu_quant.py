@@ -495,6 +495,30 @@ def test_long_calls_over_many_ranges(lrkv, lens, G, n):
     assert cache.error() == 0
 
 
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,n", [(1, 17), (1, 33), (3, 11), (5, 13), (7, 5), (33, 2), (127, 1), (1, 129),
+                                 (3, 100), (5, 52), (100, 3)])
+def test_group_sizes_of_many_rows(lrkv, code, G, n):
+    """Rows that are no power of two, in one tile and in several."""
+    cache, oc = _filled(lrkv, 3, 2, [200, 64, 331], code, seed=G)
+    _check_attention(lrkv, cache, oc, G, n, [n, n // 2, n], seed=n)
+    assert cache.error() == 0
+
+
+@pytest.mark.parametrize("B", [400, 1024])
+@pytest.mark.parametrize("G,n", [(2, 1), (4, 3), (1, 20), (2, 60), (1, 130)])
+def test_large_batches(lrkv, B, G, n):
+    """The tables of lengths take shared memory from the pages in flight."""
+    g = np.random.default_rng(B + n)
+    lens = g.integers(0, 150, B).tolist()
+    lens[0], lens[-1] = 0, 200
+    n_q = [int(x) if i % 7 == 0 or i == B - 1 else 0 for i, x in enumerate(g.integers(0, n + 1, B))]
+    n_q[-1] = n
+    cache, oc = _filled(lrkv, B, 1, lens, "int8", seed=n)
+    _check_attention(lrkv, cache, oc, G, n, n_q)
+    assert cache.error() == 0
+
+
 @pytest.mark.parametrize("n", [1, 5, 100])
 def test_the_same_call_gives_the_same_bits(lrkv, n):
     cache, oc = _filled(lrkv, 3, 2, [900, 64, 2000], "int8")
