@@ -1,8 +1,7 @@
-// Attention of 9 to 128 query rows per KV head over the 8-bit full-rank cache
+// Attention of 17 to 128 query rows per KV head over the 8-bit full-rank cache
 // (drafted tokens, short follow-ups): as many bytes as one row takes, more
-// products than mma.sync has (64 tokens of a page x 16 rows took it 1150
-// clocks per SM, the page's bytes 700), too few rows to fill a tile of
-// quant_prefill.cu.
+// than quant_decode.cu's registers hold (a warp there has the sums of all
+// rows), too few rows to fill a tile of quant_prefill.cu.
 //
 // The mathematics is quant_prefill.cu's.  The 128 rows of a tcgen05 tile are
 // REP copies of up to 128 / REP query rows; S = Q K^T of a page then stands
@@ -11,6 +10,11 @@
 // every thread keeps a running maximum and sum of its own.  P is zero outside
 // a copy's tokens (written once, at the start), so O of copy c is the sum over
 // its tokens; the copies and the two groups are added at the end of a unit.
+//
+// What bounds it: the latency of a page's way through the roles (codes, tile,
+// S, P, O).  Two pages are under way at a time and one leaves every 0.85 us,
+// 1.25 with 128 rows; its bytes would take 0.37.  4 x 8 heads x 16,384 tokens
+// (134 MB) with 20 rows 55 us, 32 rows 57, 64 rows 62, 128 rows 82.
 //
 // Persistent, one CTA per SM, 18 warps, the pages of all units dealt evenly:
 //  * warp 17: one bulk copy per page slab into a ring of NR (44 bytes a

@@ -20,6 +20,20 @@
 //    TMEM), then Q K^T of the step after the next into the S that P has just
 //    left.  (One thread for both needed 2000 clocks a step to issue what takes
 //    the tensor cores 1240.)
+// What bounds it: the softmax warps' own time.  A step of 64 keys x 256 rows
+// takes them 2000 clocks (16,384 exponentials at 16 a clock are 1024 of them;
+// the rest is TMEM's latency, the row maximum and the hand-over), the tensor
+// cores 1241.  2048 queries of 32 heads over 2 x 16,384 tokens: 1.05 ms (980
+// TFLOP/s at the clock of a cool card; 1.15 ms, 900, in a long run, at its
+// power limit); 8192 over themselves: 0.60 to 0.65 ms (910 to 855).  A tile's
+// start and end take 12 to 16 thousand clocks: 32 prompts of 512 tokens
+// 208 us (330 TFLOP/s).
+// Measured against it, the 2048 queries: two threads a row on sixteen softmax
+// warps 1.38 ms against 1.09 (what a row costs once is paid twice); a part of
+// the exponentials as polynomials on the FMA pipe 1.29 against 1.11; the next S
+// loaded ahead into registers 1.43 against 1.11; the groups started half a step
+// apart: no change, they fall into step again; separate converters of keys and
+// of values (quant_few.cu's) 1.25 against 1.23, 8K prompt 0.72 against 0.66.
 // A row keeps its references m (scores) and M' (scores + floor(log2 s_v)) as
 // long as they lag by at most 2^kLazy, so O is seldom rescaled; a weight is
 // then at most 2^(1 + kLazy + kBoostLog) = 2^15 and fp16's floor lies 2^-33
@@ -44,7 +58,9 @@ constexpr int kQGroup = 2 * kQHalf;
 // A step's scales are read until its P is written; the converters are at most
 // kRing + 2 steps ahead of that.
 constexpr int kScaleRing = 8;
-constexpr int kFar = 3;                         // steps ahead at which a page is brought into L2
+// Steps ahead at which a page is brought into L2 (256 queries over 16K, where
+// few tiles share a page: 0.39 ms without, 0.33 with; 2, 3 and 4 alike).
+constexpr int kFar = 3;
 // A tile's start and end (its rows of q and o, the empty pipeline) take about
 // as long as this many steps; the ranges count them.
 constexpr int kTileSteps = 8;

@@ -16,7 +16,6 @@ constexpr int kTileRows = 256;                  // rows of a record
 constexpr float kLazy = 6.f;
 constexpr float kBoostLog = 8.f;
 
-
 struct StepScales {
   float sk, sv;
   int ok;       // the page's tokens count
