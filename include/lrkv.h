@@ -390,8 +390,9 @@ int lrkv_dense_decode_attn(const lrkv_dense_cache *cache, const void *q,
  *
  * tail[batch][num_kv_heads][2][LRKV_QUANT_TAIL][128] bf16, keys then values:
  * token t in slot t % LRKV_QUANT_TAIL.  It holds the open block and the one
- * before it, so seq_len may be set back by up to LRKV_PAGE_TOKENS tokens
- * (drafted tokens that were rejected); the next append goes on from there.
+ * before it, so seq_len may be set back (drafted tokens that were rejected),
+ * to no more than LRKV_PAGE_TOKENS below the largest it has been; the next
+ * append goes on from there.
  *
  * The rules on block_table and append_counter are those of lrkv_cache.  The
  * kernels set *error once and never clear it: 2 = a block-table entry out of
@@ -444,8 +445,9 @@ int lrkv_quant_read(const lrkv_quant_cache *cache, const int32_t *first, int32_t
  *          h*q_head_stride + i*q_token_stride (elements, multiples of 8;
  *          likewise o); 16-byte aligned, o apart from q.  q head h reads KV head
  *          h / (num_q_heads / num_kv_heads), any whole ratio up to 128.
- *          batch * num_kv_heads * (max_pages_per_seq + 8) must fit 31 bits
- *          (LRKV_ERR_UNSUPPORTED otherwise).
+ *          batch * num_kv_heads * (max_pages_per_seq + 8) and, with R =
+ *          n_queries * that ratio, ceil(R / 256) * (max_pages_per_seq + 8)
+ *          must fit 31 bits, R 30 (LRKV_ERR_UNSUPPORTED otherwise).
  *   A key or value that is not finite makes NaN of the queries that see it
  *          (a full block's of those that see the block) and of no others.
  *   workspace : at least lrkv_quant_attn_workspace_bytes, 16-byte aligned,

@@ -33,7 +33,11 @@ int check_quant_heads(const lrkv_quant_cache* c, int H_q, int n) {
   // counted in 32 bits
   if ((long long)c->batch * c->num_kv_heads * ((long long)c->max_pages_per_seq + 8) > INT_MAX)
     return LRKV_ERR_UNSUPPORTED;
-  if ((long long)n * (H_q / c->num_kv_heads) > (1 << 30)) return LRKV_ERR_UNSUPPORTED;
+  const long long rows = (long long)n * (H_q / c->num_kv_heads);
+  if (rows > (1 << 30)) return LRKV_ERR_UNSUPPORTED;
+  // ... and so are the steps of a unit's row tiles
+  if ((rows + 255) / 256 * ((long long)c->max_pages_per_seq + 8) > INT_MAX)
+    return LRKV_ERR_UNSUPPORTED;
   return LRKV_OK;
 }
 

@@ -98,6 +98,9 @@ def test_attention_refuses_bad_calls(lrkv):
     assert call(n=1 << 30) == -2                    # rows past 32 bits
     many = ctypes.byref(_desc(lrkv, batch=1024, max_pages_per_seq=1 << 20))
     assert call(desc=many) == -2                    # blocks past 32 bits
+    long = ctypes.byref(_desc(lrkv, batch=1, num_kv_heads=1, max_pages_per_seq=65536))
+    assert call(hq=8, n=1 << 22, desc=long) == -2   # a unit's row tiles x blocks past 32 bits
+    assert L.lrkv_quant_attn_workspace_bytes(long, 8, 1 << 22) == 0
     assert call(n=0) == 0
     assert call(q=None) == -1 and call(o=None) == -1 and call(ws=None) == -1
     assert call(q=ODD) == -1 and call(o=ODD) == -1 and call(ws=ODD) == -1
