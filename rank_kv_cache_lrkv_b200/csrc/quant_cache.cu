@@ -345,8 +345,9 @@ int quant_append_launch(const QuantAppendArgs& a, cudaStream_t st) {
 }
 
 int quant_read_launch(const QuantReadArgs& a, int dtype, cudaStream_t st) {
-  const unsigned nb = (unsigned)((a.n + 62ll) / kQBlock + 1);
-  const dim3 grid(nb, a.c.H, a.c.B);
+  // blocks that n tokens can touch, and a sequence can have
+  const long long nb = (a.n + 62ll) / kQBlock + 1;
+  const dim3 grid((unsigned)(nb < a.c.maxp ? nb : a.c.maxp), a.c.H, a.c.B);
   QuantReadArgs args = a;
   void* p[] = {&args};
   const bool e = a.c.e4m3;

@@ -189,6 +189,24 @@ def test_ragged_appends_and_ranges(lrkv, code):
                     assert np.array_equal(x[b, h].cpu().numpy(), want), (n, b, h, side)
 
 
+def test_read_of_more_tokens_than_there_can_be(lrkv):
+    """Rows of tokens that do not exist are not written, so n may be anything."""
+    lens = [150, 0, 64]
+    cache, oc = _filled(lrkv, 3, 2, lens, "int8", extra=100)
+    first = [100, -7, 0]
+    k = torch.full((3, 2, 160, 128), 2.0, device="cuda")
+    v = k.clone()
+    lrkv._quant_call("lrkv_quant_read", cache, None, _counts(first).data_ptr(), 2 ** 31 - 1,
+                     k.data_ptr(), v.data_ptr(), lrkv.LRKV_F32, *k.stride()[:3])
+    for b in range(3):
+        for h in range(2):
+            for side, x in enumerate((k, v)):
+                want = np.full((160, 128), 2.0, np.float32)
+                vals = oc.values(b, h, side, np.float32)[max(first[b], 0):]
+                want[:len(vals)] = vals
+                assert np.array_equal(x[b, h].cpu().numpy(), want), (b, h, side)
+
+
 def test_read_into_rows_of_every_alignment(lrkv):
     """fp32 rows 16 bytes past a 32-byte border, by pointer and by stride."""
     cache, oc = _filled(lrkv, 1, 2, [150], "int8")
