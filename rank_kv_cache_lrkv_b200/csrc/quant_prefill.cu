@@ -200,11 +200,13 @@ __device__ __forceinline__ PrePart next_part(const Line& n, const PrePart& p, lo
 // The CTA whose range holds the place before x.
 __device__ __forceinline__ int last_cta(const Line& n, long long x) {
   const long long total = *static_cast<const volatile long long*>(&n.start[n.B]);
-  return (int)((x * min((long long)gridDim.x, total) - 1) / total);
+  const int C = (int)min((long long)gridDim.x, total);
+  const long long per = total / C, extra = total - per * C, big = extra * (per + 1);
+  return (int)(x <= big ? (x - 1) / (per + 1) : extra + (x - 1 - big) / per);
 }
 
 template <bool kE4M3>
-__global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttnArgs a, int RT) {
+__global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttnArgs a) {
   extern __shared__ __align__(1024) uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   for (int b = warp; b < c.B; b += kPreThreads / 32) {
     int s = 0;
 #pragma unroll 1
-    for (int rt = lane; rt < RT; rt += 32) s += tile_length(line, b, rt);
+    for (int rt = lane; rt * kTileRows < snq[b] * a.G; rt += 32) s += tile_length(line, b, rt);
     s = (int)__reduce_add_sync(0xffffffffu, (uint32_t)s);
     if (lane == 0) ssum[b] = s;
   }
@@ -295,9 +297,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   {
     const long long total = start[c.B];
     const int C = (int)min((long long)gridDim.x, total);
-    if ((int)blockIdx.x < C) {
-      lo = total * blockIdx.x / C;
-      hi = total * (blockIdx.x + 1) / C;
+    if ((int)blockIdx.x < C) {  // the first CTAs of a remainder take one more
+      const long long per = total / C;
+      const int extra = (int)(total - per * C);
+      lo = blockIdx.x * per + min((int)blockIdx.x, extra);
+      hi = lo + per + ((int)blockIdx.x < extra ? 1 : 0);
     }
   }
 
@@ -866,8 +870,7 @@ int quant_prefill_launch(const QuantAttnArgs& a, const DevInfo& info, cudaStream
   const int rc = prepare_kernel(fn, true);
   if (rc != LRKV_OK) return rc;
   QuantAttnArgs args = a;
-  int RT = (int)(((long long)a.n * a.G + kTileRows - 1) / kTileRows);
-  void* p[] = {&args, &RT};
+  void* p[] = {&args};
   if (launch_pdl(fn, dim3(info.sms), dim3(kPreThreads), smem, st, p) != cudaSuccess)
     return LRKV_ERR_CUDA;
   return quant_merge_launch(a, info.sms, kTileRows, st);
