@@ -46,6 +46,10 @@ namespace {
 
 constexpr int kPad = kHeadDim + 4;              // combine rows: no bank conflicts
 constexpr float kBoost = 8192.f;                // 2^13
+// What a part's end (its warps' sums, its record) takes, in blocks; the line
+// has so many places before a unit's blocks (4 x 8192 tokens 18.3 -> 17.3 us,
+// 64 x 300 28.4 -> 24.3; 3 too few, 8 the same).
+constexpr int kPartCost = 6;
 
 struct DecPlan {
   int slots, ml, full, start, len, nq, misc, total;
@@ -124,7 +128,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
   int* slen = reinterpret_cast<int*>(sm + pl.len);
   int* snq = reinterpret_cast<int*>(sm + pl.nq);
   volatile int* fail = reinterpret_cast<volatile int*>(sm + pl.misc);
-  volatile int* lastflag = fail + 1;
+  volatile int *lastflag = fail + 1, *nunits = fail + 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (threadIdx.x == 0) {
     *fail = 0;
@@ -137,12 +141,15 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
     // blocks before each sequence; a sequence without tokens still has one
     // (empty) block for its queries' zeros
     const int per = (c.B + 31) / 32, b0 = min(c.B, lane * per), b1 = min(c.B, b0 + per);
-    int own = 0;
+    int own = 0, units = 0;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       slen[b] = quant_len(c, b);
       snq[b] = quant_queries(a, b);
-      if (snq[b]) own += max(1, (slen[b] + kQBlock - 1) / kQBlock) * c.H;
+      if (snq[b]) {
+        own += (max(1, (slen[b] + kQBlock - 1) / kQBlock) + kPartCost) * c.H;
+        units += c.H;
+      }
     }
     int incl = own;
 #pragma unroll
@@ -154,14 +161,23 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       start[b] = e;
-      if (snq[b]) e += max(1, (slen[b] + kQBlock - 1) / kQBlock) * c.H;
+      if (snq[b]) e += (max(1, (slen[b] + kQBlock - 1) / kQBlock) + kPartCost) * c.H;
     }
-    if (lane == 31) start[c.B] = incl;
+    units = __reduce_add_sync(0xffffffffu, units);
+    if (lane == 31) {
+      start[c.B] = incl;
+      *nunits = units;
+    }
   }
   __syncthreads();
   const int total = start[c.B];
-  // no CTA without a block: the parts of a unit are counted as CTAs
-  const int C = min((int)gridDim.x, total);
+  // A unit's last CTA adds up its parts: no more of them than about 2 sqrt(the
+  // blocks of a unit) (a sequence's only head, 8 rows, 32,768 tokens: 19 us; a
+  // part in every CTA 32, 4 sqrt 21; 131,072 tokens 28, 33 and 34; 1 sqrt loses
+  // elsewhere, 8 heads of 8192 tokens 12.7 against 10.9).
+  const int units = *nunits;
+  const float parts = 2.f * sqrtf((float)total / max(units, 1)) + 1.f;
+  const int C = (int)min(min((long long)gridDim.x, (long long)total), (long long)(units * parts));
   if ((int)blockIdx.x >= C) return;
   // CTA i takes per blocks, the first `extra` CTAs one more
   const int per = total / C, extra = total - per * C;
@@ -179,7 +195,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
   };
   // the part after p, whose first block is the line's block p.first + p.tiles
   auto next_part = [&](Part& p) {
-    p.first += p.tiles;
+    p.first += p.tiles + kPartCost;
     if (++p.h == c.H) {
       p.h = 0;
       do ++p.b; while (start[p.b + 1] == start[p.b]);
@@ -197,8 +213,8 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
     }
     p0.b = l;
     const int tiles = max(1, (slen[l] + kQBlock - 1) / kQBlock);
-    p0.h = (lo - start[l]) / tiles;
-    p0.first = start[l] + p0.h * tiles;
+    p0.h = (lo - start[l]) / (tiles + kPartCost);
+    p0.first = start[l] + p0.h * (tiles + kPartCost) + kPartCost;
     cut(p0);
   }
 
@@ -216,7 +232,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
     while (xi < hi) {
       while (xi >= pi.first + pi.tiles) next_part(pi);
       const int i = xi - pi.first;
-      if ((i + 1) * kQBlock <= slen[pi.b]) {
+      if (i >= 0 && (i + 1) * kQBlock <= slen[pi.b]) {
         npage = __ldg(c.bt + (size_t)pi.b * c.maxp + i);
         nhead = pi.h;
         return true;
@@ -248,8 +264,38 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
     xi += W;
     more = find_next();
   };
+
+  // r / G for r < 16
+  const uint32_t inv = (65536u + a.G - 1) / a.G;
+  auto query_of = [&](int r) { return (int)((r * inv) >> 16); };
+  // row r of a part's queries
+  auto qrow = [&](const Part& p, int r) {
+    const int i = query_of(r);
+    return a.q + p.b * a.qs + (long long)(p.h * a.G + r - i * a.G) * a.qh + (long long)i * a.qt;
+  };
+  // a lane's chunks of its rows, as they are
+  uint4 qraw[NT][4];
+  auto load_q = [&](const Part& p) {
+    const int rows = snq[p.b] * a.G;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = 8 * n + g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qraw[n][i] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const uint4* src = reinterpret_cast<const uint4*>(qrow(p, r));
+        qraw[n][0] = __ldg(src + 2 * t);
+        qraw[n][1] = __ldg(src + 2 * t + 1);
+        qraw[n][2] = __ldg(src + 8 + 2 * t);
+        qraw[n][3] = __ldg(src + 9 + 2 * t);
+      }
+    }
+  };
   if (warp < W) {
     more = find_next();
+    // on its way while the first pages are asked for (4 x 8192 tokens 19.4 ->
+    // 18.4 us; two row tiles spill)
+    if constexpr (NT == 1) load_q(p0);
 #pragma unroll 1
     for (int s = 0; s < D; ++s) issue();
   }
@@ -257,19 +303,11 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
   int* counters = static_cast<int*>(a.ws);
   float* records = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + dec_records(gridDim.x));
 
-  // r / G for r < 16
-  const uint32_t inv = (65536u + a.G - 1) / a.G;
-  auto query_of = [&](int r) { return (int)((r * inv) >> 16); };
-
   Part p = p0;
   for (int x = lo; x < hi;) {
+    if (p.i1 <= 0) break;  // the range ends before the unit's first block
     const int L = slen[p.b], nq = snq[p.b], rows = nq * a.G;  // at most kRows
     const int pos0 = L - nq;  // position of query 0
-    const __nv_bfloat16* qb = a.q + p.b * a.qs + (long long)(p.h * a.G) * a.qh;
-    auto qrow = [&](int r) {
-      const int i = query_of(r);
-      return qb + (long long)(r - i * a.G) * a.qh + (long long)i * a.qt;
-    };
     float m[2 * NT], l[2 * NT], mv[2 * NT], acc[8][NT][4];
     int pos[2 * NT];
 #pragma unroll
@@ -291,7 +329,8 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
 
     if (warp < W) {
       // ---------------- quantised blocks
-      int xc = x + ((warp - (x - lo) % W) + W) % W;
+      const int xb = p.first + p.i0;
+      int xc = xb + ((warp - (xb - lo) % W) + W) % W;
       const int xend = p.first + p.i1;
       const bool have = xc < xend && (xc - p.first + 1) * kQBlock <= L;
       if (have) {
@@ -299,19 +338,10 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
         // q's B fragments, fp16, and the columns' factors
         uint32_t qf[NT][8][2];
         float fcol[2 * NT];
+        if (NT == 2 || x != lo) load_q(p);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          uint4 w[4];
-          const int r = 8 * n + g;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
-          if (r < rows) {
-            const uint4* src = reinterpret_cast<const uint4*>(qrow(r));
-            w[0] = __ldg(src + 2 * t);
-            w[1] = __ldg(src + 2 * t + 1);
-            w[2] = __ldg(src + 8 + 2 * t);
-            w[3] = __ldg(src + 9 + 2 * t);
-          }
+          const uint4(&w)[4] = qraw[n];
           uint32_t mx = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -494,7 +524,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           qw[n] = 8 * n + g < rows
-                      ? __ldg(reinterpret_cast<const uint4*>(qrow(8 * n + g)) + 4 * u4 + t)
+                      ? __ldg(reinterpret_cast<const uint4*>(qrow(p, 8 * n + g)) + 4 * u4 + t)
                       : zero;
 #pragma unroll
         for (int s4 = 0; s4 < 4; ++s4) {
@@ -679,24 +709,53 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
       }
       __syncthreads();
       if (*lastflag) {
+        // a lane weighs every 32nd part, then the warp adds them in order (a
+        // running maximum over the parts is one long chain: 52 us for the 148
+        // parts of a sequence's only head)
+        float* wt = slots + warp * kRows * kPad;  // (the slots have been read)
+        const int nc = c1 - c0 + 1;
         for (int r = warp; r < rows; r += W + 1) {
-          float4 S = make_float4(-INFINITY, 0.f, -INFINITY, 0.f), o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int cc = c0; cc <= c1; ++cc) {
-            const float4* src = record(cc, cc == c0) + r * (kPad / 4);
-            const float4 v = __ldcg(src), u = __ldcg(src + 1 + lane);
-            if (nothing(v)) continue;
-            const float mn = fmaxf(S.x, v.x), zn = fmaxf(S.z, v.z);
-            const float ref = zero_if_inf(mn), zref = zero_if_inf(zn);
-            S.y = S.y * ex2_approx(S.x - ref) + v.y * ex2_approx(v.x - ref);
-            const float f0 = ex2_approx(S.z - zref), f1 = ex2_approx(v.z - zref);
-            S.x = mn;
-            S.z = zn;
-            o.x = o.x * f0 + u.x * f1;
-            o.y = o.y * f0 + u.y * f1;
-            o.z = o.z * f0 + u.z * f1;
-            o.w = o.w * f0 + u.w * f1;
+          auto place = [&](int k) { return record(c0 + k, k == 0) + r * (kPad / 4); };
+          float4 v = make_float4(-INFINITY, 0.f, -INFINITY, 0.f), S = v, o = make_float4(0.f, 0.f, 0.f, 0.f);
+          constexpr int kFirst = NT == 1 ? 8 : 4;
+          float4 u[kFirst];  // of the first parts, asked for at once (two row tiles: 8 spill)
+#pragma unroll
+          for (int k = 0; k < kFirst; ++k)
+            if (k < nc) u[k] = __ldcg(place(k) + 1 + lane);
+          if (lane < nc) v = __ldcg(place(lane));
+          S.x = v.x;
+          S.z = v.z;
+          for (int k = lane + 32; k < nc; k += 32) {
+            const float4 y = __ldcg(place(k));
+            S.x = fmaxf(S.x, y.x);
+            S.z = fmaxf(S.z, y.z);
           }
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) {
+            S.x = fmaxf(S.x, __shfl_xor_sync(0xffffffffu, S.x, d));
+            S.z = fmaxf(S.z, __shfl_xor_sync(0xffffffffu, S.z, d));
+          }
+          const float ref = zero_if_inf(S.x), zref = zero_if_inf(S.z);
+          for (int k = lane; k < nc; k += 32) {
+            if (k >= 32) v = __ldcg(place(k));
+            wt[k] = ex2_approx(v.z - zref);
+            S.y += v.y * ex2_approx(v.x - ref);
+          }
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) S.y += __shfl_xor_sync(0xffffffffu, S.y, d);
+          __syncwarp();
+          auto add = [&](const float4& y, float f) {
+            o.x += y.x * f;
+            o.y += y.y * f;
+            o.z += y.z * f;
+            o.w += y.w * f;
+          };
+#pragma unroll
+          for (int k = 0; k < kFirst; ++k)
+            if (k < nc) add(u[k], wt[k]);
+#pragma unroll 8
+          for (int k = kFirst; k < nc; ++k) add(__ldcg(place(k) + 1 + lane), wt[k]);
+          __syncwarp();
           finish(r, S, o);
         }
       }
