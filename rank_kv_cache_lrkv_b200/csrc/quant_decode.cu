@@ -12,9 +12,9 @@
 // eleven bits down to 2^-27 of the largest.
 //
 // What bounds it: HBM for long caches (64 sequences of 12,288 tokens on
-// average x 8 heads: 1.6 GB in 274 us, 5,900 GB/s; 4 of 32,769: 49 us, 5,460),
-// latency for short ones: about 9 us between the launch and the last part
-// folded (512 tokens 9 us, 4 x 8192 21 us).  With 9 to 16 rows a page's
+// average x 8 heads: 1.6 GB in 274 us, 5,900 GB/s; 4 of 32,769: 47 us, 5,770),
+// latency for short ones: 7 to 8 us between the launch and the last part
+// folded (512 tokens 8.2 us, 4 x 8192 17.3 us).  With 9 to 16 rows a page's
 // exponentials and products take a warp longer than its bytes take to arrive:
 // 8 sequences of 12,288, 16 rows, 55 us (3,900 GB/s).
 //

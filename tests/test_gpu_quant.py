@@ -513,6 +513,16 @@ def test_long_calls_over_many_ranges(lrkv, lens, G, n):
     assert cache.error() == 0
 
 
+@pytest.mark.parametrize("L,G,n", [(20000, 8, 1), (20000, 8, 2), (9001, 1, 1), (700, 5, 3)])
+def test_the_only_head_of_a_sequence(lrkv, L, G, n):
+    """One unit over many CTAs: its parts are added up by the last of them."""
+    cache, oc = _filled(lrkv, 1, 1, [L], "int8", seed=G)
+    ws = lrkv.quant_attn_workspace(cache, G, n)
+    first = _check_attention(lrkv, cache, oc, G, n, ws=ws)
+    for _ in range(4):
+        assert torch.equal(first, _check_attention(lrkv, cache, oc, G, n, ws=ws))
+
+
 @pytest.mark.parametrize("code", ["int8", "e4m3"])
 @pytest.mark.parametrize("G,n", [(1, 17), (1, 33), (3, 11), (5, 13), (7, 5), (33, 2), (127, 1), (1, 129),
                                  (3, 100), (5, 52), (100, 3)])
