@@ -67,7 +67,7 @@ constexpr int kTileSteps = 8;
 struct PrePlan {
   int q, k, v, bars, scales, parts, misc, start, len, nq, sum, total;
 };
-constexpr int kBars = 4 * kRing + 17;
+constexpr int kBars = 2 * kRing + 17;
 __host__ __device__ inline PrePlan pre_plan(int B) {
   PrePlan p;
   p.q = 0;
@@ -214,8 +214,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   const PrePlan pl = pre_plan(c.B);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + pl.bars);
   // sfull, pfull: [group][S buffer]; odone: a step's P V ended, ofull: a part's
-  uint64_t *kfull = bars, *kempty = kfull + kRing, *vfull = kempty + kRing, *vempty = vfull + kRing,
-           *qfull = vempty + kRing, *sfull = qfull + 2, *pfull = sfull + 4, *odone = pfull + 4,
+  uint64_t *full = bars, *empty = full + kRing, *qfull = empty + kRing, *sfull = qfull + 2, *pfull = sfull + 4, *odone = pfull + 4,
            *ofull = odone + 2, *oempty = ofull + 2, *mdone = oempty + 2;
   StepScales* scales = reinterpret_cast<StepScales*>(sm + pl.scales);
   PrePart* parts = reinterpret_cast<PrePart*>(sm + pl.parts);  // [8]
@@ -230,10 +229,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   if (tid == 0) {
     *fail = 0;
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&kfull[i], 128);
-      mbar_init(&kempty[i], 2);  // both groups' issuers
-      mbar_init(&vfull[i], 128);
-      mbar_init(&vempty[i], 2);
+      mbar_init(&full[i], 4);   // the converters' warps
+      mbar_init(&empty[i], 2);  // both groups' issuers
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sfull[i], 2);  // the products' commit and the issuer itself
@@ -643,6 +640,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       if (p.j0 < j1) {
         page(p, p.j0, entry(p, p.j0));
         load_k();
+        load_v();
         next = entry(p, p.j0 + 1);
         far = entry(p, p.j0 + kFar);
       }
@@ -650,39 +648,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         const int buf = cnt % kRing;
         uint8_t* kb = sm + pl.k + buf * kTileBytes;
         uint8_t* vb = sm + pl.v + buf * kTileBytes;
-        load_v();
-        const bool open = !slab && (j + 1) * kQBlock > L;
+        const bool there = slab != nullptr, open = !there && (j + 1) * kQBlock > L;
         float sk = 1.f, sv = 1.f;
-        if (slab) {
+        int minbad = 0x7fffffff;
+        if (there) {
           sk = nsc.x;
           sv = nsc.y;
         }
-        const int ok = slab || open;
-        if (cnt >= kRing && !quant_wait_warp(&kempty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
+        if (cnt >= kRing && !quant_wait_warp(&empty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
         if (!open) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = 32 * (i >> 1) + sub;
             put_codes<kE4M3>(kb + (i & 1) * kKHalf + row * 128, row, 2 * ch, kr[i]);
           }
-        }
-        int minbad = 0x7fffffff;
-        if (open) {
+        } else {
           const int nt = L - j * kQBlock;
           int bad;
           sk = open_keys(quant_tail(c, p.b, p.h, 0, j * kQBlock), nt, kb, ct);
           sv = open_values_scale(quant_tail(c, p.b, p.h, 1, j * kQBlock), nt, ct, bad);
           if (bad < 64) minbad = j * kQBlock + bad;
         }
-        if (ct == 0) {
-          StepScales* s = &scales[cnt % kScaleRing];
-          s->sk = sk;
-          s->sv = sv;
-          s->ok = ok;
-          s->minbad = minbad;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&kfull[buf]);
         if (j + 1 < j1) {
           page(p, j + 1, next);
           load_k();
@@ -693,7 +679,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
             far = entry(p, j + 1 + kFar);
           }
         }
-        if (cnt >= kRing && !quant_wait_warp(&vempty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
         if (!open) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -701,8 +686,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         } else {
           open_values(quant_tail(c, p.b, p.h, 1, j * kQBlock), L - j * kQBlock, vb, ct, sv);
         }
+        if (j + 1 < j1) load_v();
+        if (ct == 0) {
+          StepScales* s = &scales[cnt % kScaleRing];
+          s->sk = sk;
+          s->sv = sv;
+          s->ok = there || open;
+          s->minbad = minbad;
+        }
         fence_proxy_async_smem();
-        mbar_arrive(&vfull[buf]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[buf]);
         ++cnt;
       }
     }
@@ -746,43 +740,37 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           // next step's products (V of step i, K of step i + 2) are looked at
           // before this step's products are issued, and waited for only if
           // they were not there yet.
-          auto tiles = [&](int i, bool wait) {
-            auto look = [&](uint64_t* bars, int k) {
-              uint64_t* bar = &bars[(cnt + k) % kRing];
-              const uint32_t ph = ((cnt + k) / kRing) & 1;
-              return wait ? quant_wait(bar, ph, fail) : mbar_try_wait(bar, ph);
-            };
-            const bool v = look(vfull, i);
-            return (i + 2 < n ? look(kfull, i + 2) : true) && v;
+          auto tile = [&](int i, bool wait) {
+            uint64_t* bar = &full[(cnt + i) % kRing];
+            const uint32_t ph = ((cnt + i) / kRing) & 1;
+            return wait ? quant_wait(bar, ph, fail) : mbar_try_wait(bar, ph);
           };
           if (mine > 0) ok = quant_wait(&qfull[gr], ns & 1, fail);
           for (int i = 0; i < 2 && i < n && ok; ++i) {
-            ok = quant_wait(&kfull[(cnt + i) % kRing], ((cnt + i) / kRing) & 1, fail);
+            ok = tile(i, true);
             if (!ok) break;
             tc_fence_after();
             if (i < mine) scores(i);
-            tc_commit(&kempty[(cnt + i) % kRing]);
           }
           bool seen = false;
           for (int i = 0; i < n && ok; ++i) {
             // an issuer whose group has ended keeps pace with the tiles: each
             // is given back by both, once
-            if (!seen) ok = tiles(i, true);
+            if (!seen && i + 2 < n) ok = tile(i + 2, true);
             if (ok && i < mine) {
               ok = quant_wait(&pfull[2 * gr + (i & 1)], ((np >> (i & 1)) ^ (i >> 1)) & 1, fail);
               // O's last sums have been read
               if (ok && i == 0 && ns > 0) ok = quant_wait(&oempty[gr], (ns - 1) & 1, fail);
             }
             if (!ok) break;
-            seen = i + 1 < n && tiles(i + 1, false);
+            seen = i + 3 < n && tile(i + 3, false);
             if (i < mine) {
               tc_fence_after();
               sums(i);
               if (i == mine - 1) tc_commit(&ofull[gr]);
               if (i + 2 < mine) scores(i + 2);
             }
-            tc_commit(&vempty[(cnt + i) % kRing]);
-            if (i + 2 < n) tc_commit(&kempty[(cnt + i + 2) % kRing]);
+            tc_commit(&empty[(cnt + i) % kRing]);
           }
         }
         live = __all_sync(0xffffffffu, ok);
