@@ -20,20 +20,24 @@
 //    TMEM), then Q K^T of the step after the next into the S that P has just
 //    left.  (One thread for both needed 2000 clocks a step to issue what takes
 //    the tensor cores 1240.)
-// What bounds it: the softmax warps' own time.  A step of 64 keys x 256 rows
-// takes them 2000 clocks (16,384 exponentials at 16 a clock are 1024 of them;
-// the rest is TMEM's latency, the row maximum and the hand-over), the tensor
-// cores 1241.  2048 queries of 32 heads over 2 x 16,384 tokens: 1.05 ms (980
-// TFLOP/s at the clock of a cool card; 1.15 ms, 900, in a long run, at its
-// power limit); 8192 over themselves: 0.60 to 0.65 ms (910 to 855).  A tile's
-// start and end take 12 to 16 thousand clocks: 32 prompts of 512 tokens
-// 208 us (330 TFLOP/s).
+// What bounds it: a step of 64 keys x 256 rows takes 2350 clocks, in which
+// nothing is full (tensor cores 1280, exponentials 1024, issue slots 52 %): it
+// is the chain of a step through softmax (2000: TMEM's latency, the row
+// maximum, the exponentials, the hand-over) and back through the products.  And
+// the card: in a long run it draws 990 W, its limit, at 1.78 GHz of 1.965.
+// 2048 queries of 32 heads over 2 x 16,384 tokens: 1.04 ms (990 TFLOP/s) on a
+// cool card, 1.15 ms (895) in a long run; 8192 over themselves 0.60 to 0.65 ms
+// (910 to 855).  A tile's start and end take 12 to 16 thousand clocks: 32
+// prompts of 512 tokens 200 us (340 TFLOP/s).
 // Measured against it, the 2048 queries: two threads a row on sixteen softmax
-// warps 1.38 ms against 1.09 (what a row costs once is paid twice); a part of
-// the exponentials as polynomials on the FMA pipe 1.29 against 1.11; the next S
-// loaded ahead into registers 1.43 against 1.11; the groups started half a step
-// apart: no change, they fall into step again; separate converters of keys and
-// of values (quant_few.cu's) 1.25 against 1.23, 8K prompt 0.72 against 0.66.
+// warps 1.38 ms against 1.09 (what a row costs once is paid twice); sixteen
+// warps that take a row's steps in turns 1.17 against 1.12; one S that is given
+// back as soon as it is in registers, and P of its own, 1.15 against 1.11 (8K
+// prompt 0.65 against 0.66); a part of the exponentials as polynomials on the
+// FMA pipe 1.29 against 1.11; the next S loaded ahead into registers 1.43
+// against 1.11; the groups started half a step apart: no change, they fall into
+// step again; separate converters of keys and of values (quant_few.cu's) 1.25
+// against 1.23, 8K prompt 0.72 against 0.66.
 // A row keeps its references m (scores) and M' (scores + floor(log2 s_v)) as
 // long as they lag by at most 2^kLazy, so O is seldom rescaled; a weight is
 // then at most 2^(1 + kLazy + kBoostLog) = 2^15 and fp16's floor lies 2^-33
