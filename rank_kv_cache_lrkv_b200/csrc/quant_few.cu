@@ -505,9 +505,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
           const int nt = L - j * kQBlock;
           const __nv_bfloat16 *kt = quant_tail(c, p.b, p.h, 0, j * kQBlock),
                               *vt = quant_tail(c, p.b, p.h, 1, j * kQBlock);
-          int bad;
-          sv = open_values_scale(vt, nt, ct, bad);
-          if (bad < 64) minbad = j * kQBlock + bad;
+          const float2 t = open_values_scale(vt, nt, ct);
+          sv = t.x;
+          if (__float_as_int(t.y) < 64) minbad = j * kQBlock + __float_as_int(t.y);
           if (keys) sk = open_keys(kt, nt, tile, ct);
           else open_values(vt, nt, tile, ct, sv);
         } else if (keys) {

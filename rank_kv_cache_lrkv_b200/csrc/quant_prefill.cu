@@ -668,10 +668,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           }
         } else {
           const int nt = L - j * kQBlock;
-          int bad;
           sk = open_keys(quant_tail(c, p.b, p.h, 0, j * kQBlock), nt, kb, ct);
-          sv = open_values_scale(quant_tail(c, p.b, p.h, 1, j * kQBlock), nt, ct, bad);
-          if (bad < 64) minbad = j * kQBlock + bad;
+          const float2 t = open_values_scale(quant_tail(c, p.b, p.h, 1, j * kQBlock), nt, ct);
+          sv = t.x;
+          if (__float_as_int(t.y) < 64) minbad = j * kQBlock + __float_as_int(t.y);
         }
         if (j + 1 < j1) {
           page(p, j + 1, next);

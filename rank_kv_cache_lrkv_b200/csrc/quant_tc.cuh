@@ -128,34 +128,44 @@ __device__ __forceinline__ void put_codes(uint8_t* rowp, int row, int cc, const 
 }
 
 // ---- the open block's bf16 rows as fp16 under a power of two, by the 128
-// threads ct of the converters
+// threads ct of the converters.  Real functions: once a sequence at most, and
+// in line their registers and instructions cost every page (long calls 2 to 8 %).
 // Largest finite |x| (bf16 bits) of the block's nt rows of one side and the
 // first row that is not all finite (64: none).  Every warp looks at all of
 // them: no barrier among warps that a failed wait may part.
 __device__ __forceinline__ uint32_t scan_open(const __nv_bfloat16* rows, int nt, int lane, int& bad) {
+  constexpr int kTogether = 8;  // loads on their way at once (fewer, with every
+  // element looked at alone: 168 prompts of 189 tokens 100 us against 62)
+  const uint4* src = reinterpret_cast<const uint4*>(rows) + lane;
   uint32_t mx = 0;
-  int fb = 64;
-#pragma unroll 4
-  for (int i = 0; i < 32; ++i) {
-    const int t = 2 * i + (lane >> 4);
-    if (t < nt) {
-      const uint4 w = *(reinterpret_cast<const uint4*>(rows + t * kHeadDim) + (lane & 15));
-      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll 1
+  for (int i0 = 0; 2 * i0 < nt; i0 += kTogether) {
+    uint4 w[kTogether];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+    for (int i = 0; i < kTogether; ++i)
+      w[i] = 2 * (i0 + i) + (lane >> 4) < nt ? src[32 * (i0 + i)] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int hl = 0; hl < 2; ++hl) {
-          const uint32_t x = (e[q] >> (16 * hl)) & 0x7fffu;
-          if (x < 0x7f80u) mx = max(mx, x); else fb = min(fb, t);
-        }
+    for (int i = 0; i < kTogether; ++i) {
+      mx = __vmaxu2(mx, __vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
+      mx = __vmaxu2(mx, __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
     }
   }
-  bad = (int)__reduce_min_sync(0xffffffffu, (uint32_t)fb);
+  mx = __reduce_max_sync(0xffffffffu, max(mx >> 16, mx & 0xffffu));
+  bad = 64;
+  if (mx < 0x7f80u) return mx;
+  // something is not finite: once more, element by element
+  mx = 0;
+#pragma unroll 1
+  for (int i = lane; i < nt * kHeadDim; i += 32) {
+    const uint32_t x = reinterpret_cast<const uint16_t*>(rows)[i] & 0x7fffu;
+    if (x < 0x7f80u) mx = max(mx, x); else bad = min(bad, i / kHeadDim);
+  }
+  bad = (int)__reduce_min_sync(0xffffffffu, (uint32_t)bad);
   return __reduce_max_sync(0xffffffffu, mx);
 }
 // Keys (rows: the block's first; the largest becomes 2^14 ..): writes the tile
 // kb, returns the scale.  Thread = (token, half of the dims).
-__device__ __forceinline__ float open_keys(const __nv_bfloat16* rows, int nt, uint8_t* kb, int ct) {
+static __device__ __noinline__ float open_keys(const __nv_bfloat16* rows, int nt, uint8_t* kb, int ct) {
   int bad;
   const int e = max((int)(scan_open(rows, nt, ct & 31, bad) >> 7) - 127, -100);
   const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
@@ -174,13 +184,14 @@ __device__ __forceinline__ float open_keys(const __nv_bfloat16* rows, int nt, ui
 }
 // The scale of the values (the largest becomes 2^7 ..) and the first token
 // with one that is not finite (64: none).
-__device__ __forceinline__ float open_values_scale(const __nv_bfloat16* rows, int nt, int ct, int& bad) {
+static __device__ __noinline__ float2 open_values_scale(const __nv_bfloat16* rows, int nt, int ct) {
+  int bad;
   const int e = (int)(scan_open(rows, nt, ct & 31, bad) >> 7) - 127;
-  return __uint_as_float((uint32_t)(127 - 7 + max(e, -100)) << 23);
+  return make_float2(__uint_as_float((uint32_t)(127 - 7 + max(e, -100)) << 23), __int_as_float(bad));
 }
 // Values, transposed: writes the tile vb.  Thread = dim; values that are not
 // finite become 0 (their tokens were reported).
-__device__ __forceinline__ void open_values(const __nv_bfloat16* rows, int nt, uint8_t* vb, int ct,
+static __device__ __noinline__ void open_values(const __nv_bfloat16* rows, int nt, uint8_t* vb, int ct,
                                             float sv) {
   const __nv_bfloat16* vt = rows + ct;
   const float up = __uint_as_float((254u << 23) - __float_as_uint(sv));  // 1 / sv, a power of two
