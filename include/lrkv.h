@@ -445,8 +445,8 @@ int lrkv_quant_read(const lrkv_quant_cache *cache, const int32_t *first, int32_t
  *          h*q_head_stride + i*q_token_stride (elements, multiples of 8;
  *          likewise o); 16-byte aligned, o apart from q.  q head h reads KV head
  *          h / (num_q_heads / num_kv_heads), any whole ratio up to 128.
- *          batch * num_kv_heads * (max_pages_per_seq + 8) and, with R =
- *          n_queries * that ratio, ceil(R / 256) * (max_pages_per_seq + 8)
+ *          batch * num_kv_heads * (max_pages_per_seq + 16) and, with R =
+ *          n_queries * that ratio, ceil(R / 256) * (max_pages_per_seq + 16)
  *          must fit 31 bits, R 30 (LRKV_ERR_UNSUPPORTED otherwise).
  *   A key or value that is not finite makes NaN of the queries that see it
  *          (a full block's of those that see the block) and of no others.

@@ -29,14 +29,14 @@ int check_quant(const lrkv_quant_cache* c) {
 int check_quant_heads(const lrkv_quant_cache* c, int H_q, int n) {
   if (H_q < 1 || H_q % c->num_kv_heads != 0 || n < 0) return LRKV_ERR_ARG;
   if (H_q / c->num_kv_heads > 128) return LRKV_ERR_UNSUPPORTED;
-  // blocks of the whole batch and a unit's rows (queries x grouped heads) are
-  // counted in 32 bits
-  if ((long long)c->batch * c->num_kv_heads * ((long long)c->max_pages_per_seq + 8) > INT_MAX)
+  // blocks of the whole batch (the kernels count up to 16 more a unit: what its
+  // parts cost) and a unit's rows (queries x grouped heads) are counted in 32 bits
+  if ((long long)c->batch * c->num_kv_heads * ((long long)c->max_pages_per_seq + 16) > INT_MAX)
     return LRKV_ERR_UNSUPPORTED;
   const long long rows = (long long)n * (H_q / c->num_kv_heads);
   if (rows > (1 << 30)) return LRKV_ERR_UNSUPPORTED;
   // ... and so are the steps of a unit's row tiles
-  if ((rows + 255) / 256 * ((long long)c->max_pages_per_seq + 8) > INT_MAX)
+  if ((rows + 255) / 256 * ((long long)c->max_pages_per_seq + 16) > INT_MAX)
     return LRKV_ERR_UNSUPPORTED;
   return LRKV_OK;
 }

@@ -820,9 +820,9 @@ int quant_attn_launch(const QuantAttnArgs& a, cudaStream_t st) {
   if ((long long)a.n * a.G <= kMaxRows)
     return a.c.e4m3 ? launch<true, 2, 7, 1>(a, info, st) : launch<false, 2, 7, 1>(a, info, st);
   // Up to a tile's rows in copies over the tile, against quant_prefill.cu: 4 x
-  // 16384 tokens with 20, 64 and 128 rows 55, 62 and 82 us against 82, 84 and
-  // 88; 64 x 512 with 32, 64 and 128: 57, 62 and 83 against 80, 80 and 80.
-  // (Where a CTA has one short unit 128 rows lose, 16 x 1024 tokens 47 us
+  // 16384 tokens with 20, 64 and 128 rows 55, 61 and 82 us against 82, 84 and
+  // 88; 64 x 512 with 32, 64 and 128: 56, 62 and 83 against 80, 80 and 80.
+  // (Where a CTA has one short unit 128 rows lose, 16 x 1024 tokens 46 us
   // against 38: lengths are on the device, so no rule here can tell.)
   if ((long long)a.n * a.G <= 128) return quant_few_launch(a, info, st);
   return quant_prefill_launch(a, info, st);

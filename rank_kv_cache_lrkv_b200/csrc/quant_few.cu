@@ -14,7 +14,7 @@
 // What bounds it: the latency of a page's way through the roles (codes, tile,
 // S, P, O).  Two pages are under way at a time and one leaves every 0.85 us,
 // 1.25 with 128 rows; its bytes would take 0.37.  4 x 8 heads x 16,384 tokens
-// (134 MB) with 20 rows 55 us, 32 rows 57, 64 rows 62, 128 rows 82.
+// (134 MB) with 20 rows 55 us, 32 rows 57, 64 rows 61, 128 rows 82.
 //
 // Persistent, one CTA per SM, 18 warps, the pages of all units dealt evenly:
 //  * warp 17: one bulk copy per page slab into a ring of NR (44 bytes a
@@ -35,8 +35,10 @@ namespace {
 constexpr int kFewThreads = 576;
 constexpr int kTiles = 3;        // fp16 tiles of keys, and of values, in flight
 constexpr int kFewScales = 8;    // a step's scales are read until its P is written
-// What a unit's start and end take, in steps (as in quant_prefill.cu).
-constexpr int kUnitSteps = 6;
+// What a unit's start and end take, in steps (as in quant_prefill.cu): 6, 9,
+// 12 and 16 here: 16 x 1024 tokens with 128 rows 50.6, 49.9, 47.8 and 46.0 us,
+// 4 x 16384 with 64 62.7, 61.3, 60.9 and 61.2.
+constexpr int kUnitSteps = 12;
 constexpr uint32_t kTmemP = 128, kTmemO = 256;
 
 struct FewPlan {
