@@ -741,10 +741,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
             tc_commit(&odone[gr]);
           };
           // A look at a barrier takes 200 clocks and more here (the tensor
-          // cores read shared memory most of the time), so the tiles of the
-          // next step's products (V of step i, K of step i + 2) are looked at
-          // before this step's products are issued, and waited for only if
-          // they were not there yet.
+          // cores read shared memory most of the time), so the tile of the
+          // scores after these is looked at before this step's products are
+          // issued, and waited for only if it was not there yet.
           auto tile = [&](int i, bool wait) {
             uint64_t* bar = &full[(cnt + i) % kRing];
             const uint32_t ph = ((cnt + i) / kRing) & 1;
