@@ -215,6 +215,10 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) quant_append_kern
     if (there && tid >= 32 && tid < 35) sc[2 + 3 * side + tid - 32] = 0.f;
     if (!there && tid == 0) quant_error(c, kErrBadPage);
   }
+  // A CTA is counted once all its warps have read seq_len: one without a block
+  // of its own has met no barrier before this one, and a warp that came after
+  // the new length was stored would take the call's tokens for new ones again.
+  __syncthreads();
   if (tid == 0) {
     // the last CTA of the sequence: every other has read seq_len
     __threadfence();
