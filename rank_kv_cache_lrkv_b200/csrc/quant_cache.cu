@@ -148,8 +148,9 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) quant_append_kern
         if (r0 + 16 * i < L1)
           *reinterpret_cast<uint4*>(quant_tail(c, b, h, side, r0 + 16 * i) + e) = w[i];
     }
-    if (over && tid == 0) quant_error(c, kErrCapacity);
   }
+  // (a sequence that is already full takes no token, n is 0)
+  if (over && blockIdx.x == 0 && tid == 0) quant_error(c, kErrCapacity);
 #pragma unroll 1
   for (; j < end; j += gridDim.x, it ^= 1) {
     const int pg = __ldg(c.bt + (size_t)b * c.maxp + j);

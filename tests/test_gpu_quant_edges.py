@@ -44,3 +44,31 @@ def test_short_ragged_appends_touch_no_block_past_the_end(lrkv, n):
     _write(cache, oc, lrkv, _rows(3, B, H, n), _rows(4, B, H, n), more)
     _check_values(lrkv, cache, oc)
     assert cache.error() == 0
+
+
+@pytest.mark.parametrize("n", [1, 2, 64, 128])
+def test_tokens_for_a_full_sequence_are_reported(lrkv, n):
+    """A sequence that is exactly full drops every token of the call and says
+    so; its neighbour, with room or without tokens, is untouched by that."""
+    B, H = 3, 2
+    cache = lrkv.QuantCache(B, H, 128)
+    oc = qo.QuantCacheOracle(B, H, "int8")
+    _write(cache, oc, lrkv, _rows(1, B, H, 128), _rows(2, B, H, 128), [128, 0, 128])
+    assert cache.error() == 0
+    pages, tail = cache.pages.clone(), cache.tail.clone()
+    # nothing asked of the full ones: no error
+    k, v = _rows(3, B, H, n), _rows(4, B, H, n)
+    _write(cache, oc, lrkv, k, v, [0, 0, -1])
+    assert cache.error() == 0
+    lrkv.quant_append(cache, k.cuda(), v.cuda(), n_new=_counts([n, 0, 0]))
+    assert cache.error() == 3
+    assert cache.seq_len.tolist() == [128, 0, 128]
+    assert cache.append_counter.tolist() == [0] * B
+    assert torch.equal(cache.pages, pages) and torch.equal(cache.tail, tail)
+    _check_values(lrkv, cache, oc)
+    # a decode step of the whole batch: the one with room takes its token
+    cache.error_word.zero_()
+    lrkv.quant_append(cache, k.cuda(), v.cuda())
+    oc.append(k.double().numpy(), v.double().numpy(), [0, n, 0])
+    assert cache.error() == 3
+    _check_values(lrkv, cache, oc)
