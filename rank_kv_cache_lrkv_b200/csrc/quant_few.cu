@@ -42,9 +42,9 @@ constexpr int kUnitSteps = 12;
 constexpr uint32_t kTmemP = 128, kTmemO = 256;
 
 struct FewPlan {
-  int q, k, v, ml, rowst, fc, scales, bars, rawok, misc, raw, start, len, nq, total;
+  int q, k, v, ml, rowst, fc, scales, tok, vtok, bars, rawok, misc, raw, start, len, nq, total;
 };
-constexpr int kFewBars = 4 * kTiles + 2 * 8 + 2 + 9;
+constexpr int kFewBars = 4 * kTiles + 2 * 8 + 2 + 10;
 __host__ __device__ inline FewPlan few_plan(int NR, int B) {
   FewPlan p;
   p.q = 0;
@@ -54,7 +54,9 @@ __host__ __device__ inline FewPlan few_plan(int NR, int B) {
   p.rowst = p.ml + 256 * 16;
   p.fc = p.rowst + 128 * 16;
   p.scales = p.fc + 128 * 4;
-  p.bars = p.scales + kFewScales * (int)sizeof(StepScales);
+  p.tok = p.scales + kFewScales * (int)sizeof(StepScales);
+  p.vtok = p.tok + kFewScales * kTokBytes;
+  p.bars = p.vtok + 2 * kTokValues;
   p.rawok = p.bars + kFewBars * 8;
   p.misc = p.rawok + 8 * 4;
   p.raw = (p.misc + 16 + 127) / 128 * 128;
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
   uint64_t *kfull = bars, *kempty = kfull + kTiles, *vfull = kempty + kTiles, *vempty = vfull + kTiles,
            *rawfull = vempty + kTiles, *rawempty = rawfull + 8, *sfull = rawempty + 8,
            *pfull = sfull + 2, *odone = pfull + 2, *oempty = odone + 2, *qfull = oempty + 2,
-           *qempty = qfull + 1, *mdone = qempty + 1;
+           *qempty = qfull + 1, *mdone = qempty + 1, *tokfull = mdone + 1;
   StepScales* scales = reinterpret_cast<StepScales*>(sm + pl.scales);
   volatile int* rawok = reinterpret_cast<volatile int*>(sm + pl.rawok);
   int* start = reinterpret_cast<int*>(sm + pl.start);
@@ -131,6 +133,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
     mbar_init(qfull, 128);
     mbar_init(qempty, 1);
     mbar_init(mdone, 1);
+    mbar_init(tokfull, 128);
     mbar_fence_init();
   }
   if (warp == 16) {
@@ -291,7 +294,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
         fence_proxy_async_smem();
         mbar_arrive(qfull);
       }
-      for (int k = 0; k < mine; ++k) {
+      // this group's steps but the open block's, which is a part's last
+      const int nfull = (min(n, slen[p.b] / kQBlock - p.j0) - gr + 1) >> 1;
+      for (int k = 0; k < nfull; ++k) {
         const int i = 2 * k + gr, base = (p.j0 + i) * kStepKeys + copy * CW;
         if (!quant_wait_warp(&sfull[gr], (ns + k) & 1, fail, lane)) break;
         tc_fence_after();
@@ -329,10 +334,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
           m = mn;
         }
         const bool grow = vn > mv + kLazy;
-        if (__any_sync(0xffffffffu, grow) && k > 0) {
-          if (quant_wait_warp(&odone[gr], (ns + k - 1) & 1, fail, lane)) {
+        if (__any_sync(0xffffffffu, grow)) {
+          const float cr = grow ? ex2_approx(mv - vn) : 1.f;
+          if (grow) mv = vn;
+          if (k > 0 && quant_wait_warp(&odone[gr], (ns + k - 1) & 1, fail, lane)) {
             tc_fence_after();
-            const float cr = grow ? ex2_approx(mv - vn) : 1.f;
 #pragma unroll 1
             for (int q4 = 0; q4 < 8; ++q4) {
               uint32_t o[16];
@@ -343,8 +349,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
             }
           }
         }
-        if (grow) mv = vn;
-        const float ref = m == -INFINITY ? 0.f : m, vref = mv == -INFINITY ? 0.f : mv;
+        const float ref = or_zero(m), vref = or_zero(mv);
         const float wm = fv * ex2_approx(fminf(ref + ev - vref, 112.f) + kBoostLog);
         const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f), nref = make_float2(-ref, -ref);
         float2 sum = make_float2(0.f, 0.f);
@@ -373,7 +378,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
         };
         if (edge) weigh(std::true_type()); else weigh(std::false_type());
         l += sum.x + sum.y;
-        if (sc.minbad <= pos && valid) l = NAN;  // a value row that is not finite is seen
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&pfull[gr]);
+      }
+      if (nfull < mine && quant_wait_warp(&sfull[gr], (ns + nfull) & 1, fail, lane)) {
+        const int i = 2 * nfull + gr, at = (done + i) % kFewScales;
+        tc_fence_after();
+        if (gr == 1 && nfull == 0) fcol = fc[row];
+        const RowState st = open_step({m, l, mv}, tS, tP + copy * (CW / 2), tO, CW,
+                                      sm + pl.tok + at * kTokBytes + copy * CW * 2, fcol,
+                                      pos - (p.j0 + i) * kStepKeys - copy * CW,
+                                      nfull > 0 ? &odone[gr] : nullptr, (ns + nfull - 1) & 1, fail);
+        m = st.m;
+        mv = st.mv;
+        l = st.l;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&pfull[gr]);
@@ -465,54 +484,51 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
     const int ct = (tid - 256) & 127, sub = ct >> 2, ch = ct & 3;  // 32 rows x 4 chunks a round
     uint64_t* tfull = keys ? kfull : vfull;
     uint64_t* tempty = keys ? kempty : vempty;
-    uint32_t cnt = 0, tph = 1, rph = 0;  // steps converted; phases of the tiles and the ring
+    // steps converted, and open blocks; phases of the tiles and the ring
+    uint32_t cnt = 0, opens = 0, tph = 1, rph = 0;
     int buf = 0, rs = 0;
     bool live = true;
     for (int x = lo; x < hi && live; advance(p, x)) {
       const int L = slen[p.b];
-      for (int j = p.j0; j < p.j1; ++j, ++cnt) {
-        const bool full = (j + 1) * kQBlock <= L, open = !full && j * kQBlock < L;
+      auto written = [&]() {
+        fence_proxy_async_smem();
+        mbar_arrive(&tfull[buf]);
+        ++cnt;
+        if (++buf == kTiles) {
+          buf = 0;
+          tph ^= 1;
+        }
+      };
+      const int jf = min(p.j1, L / kQBlock);  // full blocks; then the open one
+      for (int j = p.j0; j < jf; ++j) {
         const uint8_t* raw = sm + pl.raw + rs * kQSlab;
         uint8_t* tile = sm + (keys ? pl.k : pl.v) + buf * kTileBytes;
-        bool there = false;
         uint4 w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
         float sk = 1.f, sv = 1.f;
-        int minbad = 0x7fffffff;
-        if (full) {
-          if (!quant_wait_warp(&rawfull[rs], rph, fail, lane)) { live = false; break; }
-          there = rawok[rs] != 0;  // if not, zeros under weights of zero
-          if (there) {
+        if (!quant_wait_warp(&rawfull[rs], rph, fail, lane)) { live = false; break; }
+        const bool there = rawok[rs] != 0;  // if not, zeros under weights of zero
+        if (there) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = *reinterpret_cast<const uint4*>(
-                  raw + (keys ? quant_k_chunk(32 * (i >> 1) + sub, ch + 4 * (i & 1))
-                              : kQSide + (32 * i + sub) * kQBlock + ch * 16));
-            if (keys && ct == 0) {
-              const float2 t = *reinterpret_cast<const float2*>(raw + 2 * kQSide);
-              sk = t.x;
-              sv = t.y;
-            }
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&rawempty[rs]);  // the codes are in registers
-          if (++rs == NR) {
-            rs = 0;
-            rph ^= 1;
+          for (int i = 0; i < 4; ++i)
+            w[i] = *reinterpret_cast<const uint4*>(
+                raw + (keys ? quant_k_chunk(32 * (i >> 1) + sub, ch + 4 * (i & 1))
+                            : kQSide + (32 * i + sub) * kQBlock + ch * 16));
+          if (keys && ct == 0) {
+            const float2 t = *reinterpret_cast<const float2*>(raw + 2 * kQSide);
+            sk = t.x;
+            sv = t.y;
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rawempty[rs]);  // the codes are in registers
+        if (++rs == NR) {
+          rs = 0;
+          rph ^= 1;
+        }
         if (!quant_wait_warp(&tempty[buf], tph, fail, lane)) { live = false; break; }
-        if (open) {
-          const int nt = L - j * kQBlock;
-          const __nv_bfloat16 *kt = quant_tail(c, p.b, p.h, 0, j * kQBlock),
-                              *vt = quant_tail(c, p.b, p.h, 1, j * kQBlock);
-          const float2 t = open_values_scale(vt, nt, ct);
-          sv = t.x;
-          if (__float_as_int(t.y) < 64) minbad = j * kQBlock + __float_as_int(t.y);
-          if (keys) sk = open_keys(kt, nt, tile, ct);
-          else open_values(vt, nt, tile, ct, sv);
-        } else if (keys) {
+        if (keys) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = 32 * (i >> 1) + sub;
@@ -527,15 +543,28 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
           StepScales* s = &scales[cnt % kFewScales];
           s->sk = sk;
           s->sv = sv;
-          s->ok = there || open;
-          s->minbad = minbad;
+          s->ok = there ? 1 : 0;
         }
-        fence_proxy_async_smem();
-        mbar_arrive(&tfull[buf]);
-        if (++buf == kTiles) {
-          buf = 0;
-          tph ^= 1;
+        written();
+      }
+      if (live && jf < p.j1) {  // (of an empty sequence too: no rows of it)
+        if (!quant_wait_warp(&tempty[buf], tph, fail, lane)) { live = false; break; }
+        const int nt = L - jf * kQBlock;
+        const __nv_bfloat16 *kt = quant_tail(c, p.b, p.h, 0, jf * kQBlock),
+                            *vt = quant_tail(c, p.b, p.h, 1, jf * kQBlock);
+        uint8_t* tile = sm + (keys ? pl.k : pl.v) + buf * kTileBytes;
+        // (the values' exponents: the keys' converters' for the softmax, the values' own)
+        uint8_t* tok = keys ? sm + pl.tok + cnt % kFewScales * kTokBytes : sm + pl.vtok + (opens & 1) * kTokValues;
+        open_value_exponents(vt, nt, ct, tok);
+        if (keys) {
+          open_keys(kt, nt, tile, ct, tok);
+        } else {
+          mbar_arrive(tokfull);
+          if (!quant_wait_warp(tokfull, opens & 1, fail, lane)) { live = false; break; }
+          ++opens;
+          open_values(vt, nt, tile, ct, tok);
         }
+        written();
       }
     }
   } else if (warp == 16) {

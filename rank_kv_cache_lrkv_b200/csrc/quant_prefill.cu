@@ -15,7 +15,7 @@
 //  * warps 8-11: converters.  Codes from L2 into registers a step ahead, two
 //    bytes to two fp16 numbers, into the 128-byte-swizzled K-major tiles
 //    (keys as rows for Q K^T; the stored transpose of V is already K-major
-//    for P V).  The open block's bf16 rows become fp16 under a power of two.
+//    for P V).  The open block's rows become fp16 under a power of two each.
 //  * warps 12 and 13, one lane each, for group 0 and 1: per step P V (A from
 //    TMEM), then Q K^T of the step after the next into the S that P has just
 //    left.  (One thread for both needed 2000 clocks a step to issue what takes
@@ -70,9 +70,9 @@ constexpr int kFar = 3;
 // 189 tokens 65, 62 and 54 us, one of 8192 604, 610 and 626.)
 constexpr int kTileSteps = 8;
 struct PrePlan {
-  int q, k, v, bars, scales, parts, misc, start, len, nq, sum, total;
+  int q, k, v, bars, scales, tok, parts, misc, start, len, nq, sum, total;
 };
-constexpr int kBars = 2 * kRing + 17;
+constexpr int kBars = 2 * kRing + 18;
 __host__ __device__ inline PrePlan pre_plan(int B) {
   PrePlan p;
   p.q = 0;
@@ -80,7 +80,8 @@ __host__ __device__ inline PrePlan pre_plan(int B) {
   p.v = p.k + kRing * kTileBytes;
   p.bars = p.v + kRing * kTileBytes;
   p.scales = (p.bars + kBars * 8 + 15) / 16 * 16;
-  p.parts = p.scales + kScaleRing * (int)sizeof(StepScales);
+  p.tok = p.scales + kScaleRing * (int)sizeof(StepScales);
+  p.parts = p.tok + kScaleRing * kTokBytes;
   p.misc = p.parts + 8 * 48;
   p.start = p.misc + 64;
   p.sum = p.start + (B + 1) * 8;
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + pl.bars);
   // sfull, pfull: [group][S buffer]; odone: a step's P V ended, ofull: a part's
   uint64_t *full = bars, *empty = full + kRing, *qfull = empty + kRing, *sfull = qfull + 2, *pfull = sfull + 4, *odone = pfull + 4,
-           *ofull = odone + 2, *oempty = ofull + 2, *mdone = oempty + 2;
+           *ofull = odone + 2, *oempty = ofull + 2, *mdone = oempty + 2, *tokfull = mdone + 1;
   StepScales* scales = reinterpret_cast<StepScales*>(sm + pl.scales);
   PrePart* parts = reinterpret_cast<PrePart*>(sm + pl.parts);  // [8]
   long long* start = reinterpret_cast<long long*>(sm + pl.start);
@@ -248,6 +249,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       mbar_init(&oempty[i], 128);
     }
     mbar_init(mdone, 2);
+    mbar_init(tokfull, 128);
     mbar_fence_init();
   }
   pdl_trigger();
@@ -331,22 +333,22 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       __syncwarp();
     }
     for (long long x = lo; x < hi;) {
-      float m = -INFINITY, l = 0.f, mv = -INFINITY;
-      int n;  // this group's steps here
+      float m = -INFINITY, l = 0.f, mv = -INFINITY, fcol = 0.f;
+      int pos;
       {
         const PrePart p = parts[warp];
         const int nq = snq[p.b], pos0 = slen[p.b] - nq;
         const int rr = p.r0 + gr * 128 + row;
-        const int pos = rr < nq * a.G ? pos0 + div_group(a, rr) : 0x7fffffff;
+        pos = rr < nq * a.G ? pos0 + div_group(a, rr) : 0x7fffffff;
         const int minpos = pos0 + div_group(a, p.r0 + gr * 128);
-        n = min(p.j1, p.ntile(gr)) - p.j0;
+        // this group's steps here, and those but the open block's
+        int n = min(p.j1, p.ntile(gr)) - p.j0;
         const uint32_t steps = max(0, min(p.j1, max(p.nt0, p.nt1)) - p.j0);
         if (n > 0) {
         // ---- q: the warp copies its 32 rows as they are to where they belong
         // (two rows at a time, chunks of 16 bytes turned by the row), each
         // thread then turns its own row into fp16 with its largest element in
         // [2^14, 2^15)
-        float fcol;
         {
           const int w0 = row & ~31, R = nq * a.G, ch = lane & 15;
           int r = p.r0 + gr * 128 + w0 + (lane >> 4);
@@ -405,6 +407,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         }
         fence_proxy_async_smem();
         mbar_arrive(&qfull[gr]);
+        n = min(n, slen[p.b] / kQBlock - p.j0);
         for (int i = 0; i < n; ++i) {
           const int base = (p.j0 + i) * kStepKeys, sb = i & 1;
           if (!quant_wait_warp(&sfull[2 * gr + sb], (ns >> sb) & 1, fail, lane)) break;
@@ -447,11 +450,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
             m = mn;
           }
           const bool grow = vn > mv + kLazy;
-          if (__any_sync(0xffffffffu, grow) && i > 0) {
+          if (__any_sync(0xffffffffu, grow)) {
+            const float cr = grow ? ex2_approx(mv - vn) : 1.f;
+            if (grow) mv = vn;
             // the step before has been added; this one waits for P
-            if (quant_wait_warp(&odone[gr], (nd + i - 1) & 1, fail, lane)) {
+            if (i > 0 && quant_wait_warp(&odone[gr], (nd + i - 1) & 1, fail, lane)) {
               tc_fence_after();
-              const float cr = grow ? ex2_approx(mv - vn) : 1.f;
 #pragma unroll 1
               for (int q4 = 0; q4 < 8; ++q4) {
                 uint32_t o[16];
@@ -462,9 +466,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
               }
             }
           }
-          if (grow) mv = vn;
-          const float ref = m == -INFINITY ? 0.f : m, vref = mv == -INFINITY ? 0.f : mv;
-          // 2^(m - M') s_v 2^kBoostLog (no more than 2^126: p is 0 there)
+          const float ref = or_zero(m), vref = or_zero(mv);
+          // 2^(m - M') s_v 2^kBoostLog
           const float wm = fv * ex2_approx(fminf(ref + ev - vref, 112.f) + kBoostLog);
           const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f), nref = make_float2(-ref, -ref);
           float2 sum = make_float2(0.f, 0.f);
@@ -493,9 +496,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           };
           if (edge) weigh(std::true_type()); else weigh(std::false_type());
           l += sum.x + sum.y;
-          // a value row that is not finite is seen (in rows that are not
-          // there, always: nobody reads them)
-          if (sc.minbad <= pos) l = NAN;
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&pfull[2 * gr + sb]);
@@ -503,8 +503,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         }
         done += steps;
       }
-      // ---- the row's sums (no registers for its place in the loop above)
+      // ---- the open block, and the row's sums (no registers for its place in the
+      // loop above)
       PrePart p = parts[warp];
+      const int n = min(p.j1, p.ntile(gr)) - p.j0, nopen = slen[p.b] / kQBlock - p.j0;
+      if (nopen < n) {
+        const int sb = nopen & 1, at = (done - 1) % kScaleRing;
+        const uint32_t tSb = tS + 64 * sb;
+        if (quant_wait_warp(&sfull[2 * gr + sb], (ns >> sb) & 1, fail, lane)) {
+          ns ^= 1u << sb;
+          tc_fence_after();
+          const RowState r = open_step({m, l, mv}, tSb, tSb, tO, kStepKeys, sm + pl.tok + at * kTokBytes,
+                                       fcol, pos - (p.j0 + nopen) * kStepKeys,
+                                       nopen > 0 ? &odone[gr] : nullptr, (nd + nopen - 1) & 1, fail);
+          m = r.m;
+          l = r.l;
+          mv = r.mv;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&pfull[2 * gr + sb]);
+        }
+      }
       if (p.j1 > p.j0) {
       float4* records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.ws) + pre_records(gridDim.x));
       const bool whole = p.j0 == 0 && p.j1 == p.steps;
@@ -603,7 +622,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     const int ct = tid - 256;
     const int sub = ct >> 2, ch = ct & 3;  // 32 rows x 4 chunks a round
     uint4 kr[4], vr[4];
-    uint32_t cnt = 0;     // steps converted
+    uint32_t cnt = 0, opens = 0;  // steps converted, and open blocks
     const uint8_t* slab;  // slab of a step (nullptr: open, or out of range)
     float2 nsc;           // its scales
     int next = 0, far = 0;  // table entries of the steps j + 1 and j + kFar
@@ -641,64 +660,67 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     if (lo < hi) p = find_part(line, lo, hi);
     for (long long x = lo; x < hi && live; advance(p, x)) {
       const int L = slen[p.b], last = max(p.nt0, p.nt1);
-      const int j1 = min(p.j1, last);
-      if (p.j0 < j1) {
+      const int j1 = min(p.j1, last), jf = min(j1, L / kQBlock);  // full blocks; then the open one
+      if (p.j0 < jf) {
         page(p, p.j0, entry(p, p.j0));
         load_k();
         load_v();
         next = entry(p, p.j0 + 1);
         far = entry(p, p.j0 + kFar);
       }
-      for (int j = p.j0; j < j1; ++j) {
+      for (int j = p.j0; j < jf; ++j) {
         const int buf = cnt % kRing;
         uint8_t* kb = sm + pl.k + buf * kTileBytes;
         uint8_t* vb = sm + pl.v + buf * kTileBytes;
-        const bool there = slab != nullptr, open = !there && (j + 1) * kQBlock > L;
+        const bool there = slab != nullptr;
         float sk = 1.f, sv = 1.f;
-        int minbad = 0x7fffffff;
         if (there) {
           sk = nsc.x;
           sv = nsc.y;
         }
         if (cnt >= kRing && !quant_wait_warp(&empty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
-        if (!open) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = 32 * (i >> 1) + sub;
-            put_codes<kE4M3>(kb + (i & 1) * kKHalf + row * 128, row, 2 * ch, kr[i]);
-          }
-        } else {
-          const int nt = L - j * kQBlock;
-          sk = open_keys(quant_tail(c, p.b, p.h, 0, j * kQBlock), nt, kb, ct);
-          const float2 t = open_values_scale(quant_tail(c, p.b, p.h, 1, j * kQBlock), nt, ct);
-          sv = t.x;
-          if (__float_as_int(t.y) < 64) minbad = j * kQBlock + __float_as_int(t.y);
+        for (int i = 0; i < 4; ++i) {
+          const int row = 32 * (i >> 1) + sub;
+          put_codes<kE4M3>(kb + (i & 1) * kKHalf + row * 128, row, 2 * ch, kr[i]);
         }
-        if (j + 1 < j1) {
+        if (j + 1 < jf) {
           page(p, j + 1, next);
           load_k();
           next = entry(p, j + 2);
           if (ct == 0) {
-            if (j + kFar < j1 && far >= 0 && far < c.num_pages)
+            if (j + kFar < jf && far >= 0 && far < c.num_pages)
               l2_prefetch(c.pages + ((size_t)far * c.H + p.h) * kQSlab, kQSlab);
             far = entry(p, j + 1 + kFar);
           }
         }
-        if (!open) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            put_codes<kE4M3>(vb + (32 * i + sub) * 128, 32 * i + sub, 2 * ch, vr[i]);
-        } else {
-          open_values(quant_tail(c, p.b, p.h, 1, j * kQBlock), L - j * kQBlock, vb, ct, sv);
-        }
-        if (j + 1 < j1) load_v();
+        for (int i = 0; i < 4; ++i)
+          put_codes<kE4M3>(vb + (32 * i + sub) * 128, 32 * i + sub, 2 * ch, vr[i]);
+        if (j + 1 < jf) load_v();
         if (ct == 0) {
           StepScales* s = &scales[cnt % kScaleRing];
           s->sk = sk;
           s->sv = sv;
-          s->ok = there || open;
-          s->minbad = minbad;
+          s->ok = there ? 1 : 0;
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[buf]);
+        ++cnt;
+      }
+      if (live && jf < j1) {  // no pages' registers are held here
+        const int buf = cnt % kRing, nt = L - jf * kQBlock;
+        uint8_t* tok = sm + pl.tok + cnt % kScaleRing * kTokBytes;
+        const __nv_bfloat16 *kt = quant_tail(c, p.b, p.h, 0, jf * kQBlock),
+                            *vt = quant_tail(c, p.b, p.h, 1, jf * kQBlock);
+        if (cnt >= kRing && !quant_wait_warp(&empty[buf], (cnt / kRing - 1) & 1, fail, lane)) { live = false; break; }
+        open_value_exponents(vt, nt, ct, tok);
+        mbar_arrive(tokfull);
+        open_keys(kt, nt, sm + pl.k + buf * kTileBytes, ct, tok);
+        if (!quant_wait_warp(tokfull, opens & 1, fail, lane)) { live = false; break; }
+        ++opens;
+        open_values(vt, nt, sm + pl.v + buf * kTileBytes, ct, tok);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[buf]);

@@ -16,11 +16,15 @@ constexpr int kTileRows = 256;                  // rows of a record
 constexpr float kLazy = 6.f;
 constexpr float kBoostLog = 8.f;
 
-struct StepScales {
+struct alignas(16) StepScales {
   float sk, sv;
   int ok;       // the page's tokens count
-  int minbad;   // first open token whose value row is not finite
 };
+// The open block's tokens have powers of two of their own (so that no token takes
+// bits from others, least of all from those of queries that do not see it): the
+// exponents of their values (NaN: one is not finite), then the powers of their keys,
+// all bf16 numbers.
+constexpr int kTokValues = 2 * kStepKeys, kTokBytes = 2 * kTokValues;
 
 // Workspace: the counters of the few-row kernel (not used here, and left
 // alone), a cut per CTA (sequence, head, row and last CTA of the tile that
@@ -106,6 +110,20 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&v)[8]) 
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+// 8 consecutive columns of this thread's lane, and the wait for them.
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])::
+                   "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -127,76 +145,85 @@ __device__ __forceinline__ void put_codes(uint8_t* rowp, int row, int cc, const 
       make_uint4(h[4], h[5], h[6], h[7]);
 }
 
-// ---- the open block's bf16 rows as fp16 under a power of two, by the 128
-// threads ct of the converters.  Real functions: once a sequence at most, and
-// in line their registers and instructions cost every page (long calls 2 to 8 %).
-// Largest finite |x| (bf16 bits) of the block's nt rows of one side and the
-// first row that is not all finite (64: none).  Every warp looks at all of
-// them: no barrier among warps that a failed wait may part.
-__device__ __forceinline__ uint32_t scan_open(const __nv_bfloat16* rows, int nt, int lane, int& bad) {
-  constexpr int kTogether = 8;  // loads on their way at once (fewer, with every
-  // element looked at alone: 168 prompts of 189 tokens 100 us against 62)
-  const uint4* src = reinterpret_cast<const uint4*>(rows) + lane;
-  uint32_t mx = 0;
-#pragma unroll 1
-  for (int i0 = 0; 2 * i0 < nt; i0 += kTogether) {
-    uint4 w[kTogether];
-#pragma unroll
-    for (int i = 0; i < kTogether; ++i)
-      w[i] = 2 * (i0 + i) + (lane >> 4) < nt ? src[32 * (i0 + i)] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < kTogether; ++i) {
-      mx = __vmaxu2(mx, __vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
-      mx = __vmaxu2(mx, __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-    }
-  }
-  mx = __reduce_max_sync(0xffffffffu, max(mx >> 16, mx & 0xffffu));
-  bad = 64;
-  if (mx < 0x7f80u) return mx;
-  // something is not finite: once more, element by element
-  mx = 0;
-#pragma unroll 1
-  for (int i = lane; i < nt * kHeadDim; i += 32) {
-    const uint32_t x = reinterpret_cast<const uint16_t*>(rows)[i] & 0x7fffu;
-    if (x < 0x7f80u) mx = max(mx, x); else bad = min(bad, i / kHeadDim);
-  }
-  bad = (int)__reduce_min_sync(0xffffffffu, (uint32_t)bad);
-  return __reduce_max_sync(0xffffffffu, mx);
+// ---- the open block's bf16 rows as fp16 under a power of two for each row, by
+// the 128 threads ct of the converters.  Real functions: once a sequence at most,
+// and in line their registers and instructions cost every page (long calls 2 to 8 %).
+// Short ones: code that is run through a single time is waited for, 16 bytes an
+// instruction (64 rows of values unrolled, 168 prompts of 189 tokens 150 us, so 91).
+__device__ __forceinline__ uint32_t abs_max8(const uint4& w) {  // bf16 bits
+  const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                              __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+  return max(m >> 16, m & 0xffffu);
 }
-// Keys (rows: the block's first; the largest becomes 2^14 ..): writes the tile
-// kb, returns the scale.  Thread = (token, half of the dims).
-static __device__ __noinline__ float open_keys(const __nv_bfloat16* rows, int nt, uint8_t* kb, int ct) {
-  int bad;
-  const int e = max((int)(scan_open(rows, nt, ct & 31, bad) >> 7) - 127, -100);
-  const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-  const int tok = ct >> 1, side = ct & 1;
-  const uint4* src = reinterpret_cast<const uint4*>(rows + tok * kHeadDim) + 8 * side;
+// Largest |x| (bf16 bits) of row ct / 2 of the block's rows, nt of them.
+static __device__ __noinline__ uint32_t open_row_max(const __nv_bfloat16* rows, int nt, int ct) {
+  const uint4* src = reinterpret_cast<const uint4*>(rows + (ct >> 1) * kHeadDim) + 8 * (ct & 1);
+  uint4 w[8];
 #pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = (ct >> 1) < nt ? src[i] : make_uint4(0, 0, 0, 0);
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx = max(mx, abs_max8(w[i]));
+  return max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+}
+// Keys (a row's largest finite element becomes 2^14 ..): writes the tile kb and the
+// tokens' powers of two.  Thread = (token, half of the dims).
+static __device__ __noinline__ void open_keys(const __nv_bfloat16* rows, int nt, uint8_t* kb, int ct,
+                                              uint8_t* tok) {
+  const int t = ct >> 1, side = ct & 1;
+  uint32_t mx = open_row_max(rows, nt, ct);
+  if (__any_sync(0xffffffffu, mx >= 0x7f80u)) {  // what is not finite does not count
+    mx = 0;
+#pragma unroll 1
+    for (int i = 0; i < 64 && t < nt; ++i) {
+      const uint32_t x = reinterpret_cast<const uint16_t*>(rows)[t * kHeadDim + 64 * side + i] & 0x7fffu;
+      if (x < 0x7f80u) mx = max(mx, x);
+    }
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  }
+  const int byte = max((int)(mx >> 7) - 14, 13);  // 127 - 14 + the exponent, at least -100
+  if (side == 0) reinterpret_cast<uint16_t*>(tok + kTokValues)[t] = (uint16_t)(byte << 7);
+  const float up = __uint_as_float((uint32_t)(254 - byte) << 23);
+  const uint4* src = reinterpret_cast<const uint4*>(rows + t * kHeadDim) + 8 * side;
+#pragma unroll 2
   for (int i = 0; i < 8; ++i) {
-    const uint4 w = tok < nt ? src[i] : make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(kb + side * kKHalf + tok * 128 + ((i ^ (tok & 7)) << 4)) =
+    const uint4 w = t < nt ? src[i] : make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(kb + side * kKHalf + t * 128 + ((i ^ (t & 7)) << 4)) =
         make_uint4(pack_h2(bf_lo(w.x) * up, bf_hi(w.x) * up),
                    pack_h2(bf_lo(w.y) * up, bf_hi(w.y) * up),
                    pack_h2(bf_lo(w.z) * up, bf_hi(w.z) * up),
                    pack_h2(bf_lo(w.w) * up, bf_hi(w.w) * up));
   }
-  return __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 }
-// The scale of the values (the largest becomes 2^7 ..) and the first token
-// with one that is not finite (64: none).
-static __device__ __noinline__ float2 open_values_scale(const __nv_bfloat16* rows, int nt, int ct) {
-  int bad;
-  const int e = (int)(scan_open(rows, nt, ct & 31, bad) >> 7) - 127;
-  return make_float2(__uint_as_float((uint32_t)(127 - 7 + max(e, -100)) << 23), __int_as_float(bad));
+// The exponents of the values (a row's largest element becomes 2^7 ..).
+__device__ __forceinline__ void open_value_exponents(const __nv_bfloat16* rows, int nt, int ct, uint8_t* tok) {
+  const uint32_t mx = open_row_max(rows, nt, ct);
+  const float e = mx < 0x7f80u ? (float)(max((int)(mx >> 7) - 127, -100) - 7) : NAN;
+  if (!(ct & 1)) reinterpret_cast<uint16_t*>(tok)[ct >> 1] = (uint16_t)(__float_as_uint(e) >> 16);
 }
-// Values, transposed: writes the tile vb.  Thread = dim; values that are not
-// finite become 0 (their tokens were reported).
+// Eight of the tokens' numbers.
+struct Tok8 {
+  uint32_t w[4];
+  __device__ __forceinline__ explicit Tok8(const uint8_t* p) {
+    const uint4 t = *reinterpret_cast<const uint4*>(p);
+    w[0] = t.x;
+    w[1] = t.y;
+    w[2] = t.z;
+    w[3] = t.w;
+  }
+  __device__ __forceinline__ float operator[](int k) const { return k & 1 ? bf_hi(w[k >> 1]) : bf_lo(w[k >> 1]); }
+};
+__device__ __forceinline__ float exp2_whole(float x) {  // 2^x, x whole: in the last bits of x + 1.5 2^23 + 127
+  return __uint_as_float(__float_as_uint(x + (12582912.f + 127.f)) << 23);
+}
+// Values, transposed, by all tokens' exponents: writes the tile vb.  Thread = dim; rows
+// with a value that is not finite become 0.
 static __device__ __noinline__ void open_values(const __nv_bfloat16* rows, int nt, uint8_t* vb, int ct,
-                                            float sv) {
+                                                const uint8_t* tok) {
   const __nv_bfloat16* vt = rows + ct;
-  const float up = __uint_as_float((254u << 23) - __float_as_uint(sv));  // 1 / sv, a power of two
 #pragma unroll 1
   for (int cc = 0; cc < 8; ++cc) {
+    const Tok8 ev(tok + 16 * cc);
     uint32_t h[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -204,14 +231,88 @@ static __device__ __noinline__ void open_values(const __nv_bfloat16* rows, int n
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int t = 8 * cc + 2 * q + e;
-        v[e] = t < nt ? __bfloat162float(vt[t * kHeadDim]) * up : 0.f;
-        if (!(fabsf(v[e]) < 1e30f)) v[e] = 0.f;
+        const float x = ev[2 * q + e];
+        v[e] = t < nt && x == x ? __bfloat162float(vt[t * kHeadDim]) * exp2_whole(-x) : 0.f;
       }
       h[q] = pack_h2(v[0], v[1]);
     }
-    *reinterpret_cast<uint4*>(vb + ct * 128 + ((cc ^ (ct & 7)) << 4)) =
-        make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(vb + ct * 128 + ((cc ^ (ct & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
   }
+}
+
+// ---- the softmax of the open block
+//
+// A real function over S in TMEM: it is called once a part, in line it spills.
+__device__ __forceinline__ float or_zero(float x) { return x == -INFINITY ? 0.f : x; }
+// A row's state, and the open block's step: the columns of S up to `last`, P, O
+// (whose last sums `odone` tells of; nullptr: there are none yet).  tok: the
+// columns' tokens, fcol: the row's factor.
+struct RowState {
+  float m, l, mv;
+};
+static __device__ __noinline__ RowState open_step(RowState r, uint32_t tS, uint32_t tP, uint32_t tO,
+                                                  int columns, const uint8_t* tok, float fcol, int last,
+                                                  uint64_t* odone, uint32_t parity, volatile int* fail) {
+  // scores, back to where S was (masked: -inf); the largest, and the largest score +
+  // exponent of the value
+  float mn = -INFINITY, vn = -INFINITY;
+#pragma unroll 1
+  for (int k0 = 0; k0 < columns; k0 += 8) {
+    uint32_t s[8];
+    tmem_ld8(tS + k0, s);
+    const Tok8 ev(tok + 2 * k0), kf(tok + kTokValues + 2 * k0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float x = __fmul_rn(__uint_as_float(s[k]), fcol * kf[k]);
+      if (k0 + k > last) x = -INFINITY;
+      mn = fmaxf(mn, x);
+      vn = fmaxf(vn, x + ev[k]);
+      s[k] = __float_as_uint(x);
+    }
+    tmem_st8(tS + k0, s);
+  }
+  if (mn > r.m + kLazy) {
+    r.l *= ex2_approx(r.m - mn);
+    r.m = mn;
+  }
+  const bool grow = vn > r.mv + kLazy;
+  const float cr = grow ? ex2_approx(r.mv - vn) : 1.f;
+  if (grow) r.mv = vn;
+  if (__any_sync(0xffffffffu, grow) && odone && quant_wait_warp(odone, parity, fail, threadIdx.x & 31)) {
+    tc_fence_after();
+#pragma unroll 1
+    for (int q4 = 0; q4 < 8; ++q4) {
+      uint32_t o[16];
+      tmem_ld16(tO + 16 * q4, o);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * cr);
+      tmem_st16(tO + 16 * q4, o);
+    }
+  }
+  tmem_wait_st();
+  const float ref = or_zero(r.m), c = ref - or_zero(r.mv) + kBoostLog;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int k0 = 0; k0 < columns; k0 += 8) {
+    uint32_t s[8], pk[4];
+    tmem_ld8(tS + k0, s);
+    const Tok8 ev(tok + 2 * k0);
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      float w[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float x = __uint_as_float(s[k + u]) - ref;
+        sum += ex2_approx(x);
+        // (NaN of a value that is not finite does not reach what is masked)
+        w[u] = k0 + k + u > last ? 0.f : ex2_approx(x + (c + ev[k + u]));
+      }
+      pk[k >> 1] = pack_h2(w[0], w[1]);
+    }
+    tmem_st4(tP + (k0 >> 1), pk);
+  }
+  r.l += sum;
+  return r;
 }
 
 // Parts of cut tiles, folded (quant_prefill.cu); rows: rows of a tile in use.

@@ -1,10 +1,11 @@
 """The 8-bit cache on the GPU where calls meet their limits: CTAs without
 blocks, full sequences, open tokens far from their neighbours."""
+import numpy as np
 import pytest
 import torch
 
 from oracle import quant_oracle as qo
-from tests.test_gpu_quant import _check_values, _counts, _rows, _write
+from tests.test_gpu_quant import SCALE, _check_values, _counts, _rows, _write
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +73,95 @@ def test_tokens_for_a_full_sequence_are_reported(lrkv, n):
     oc.append(k.double().numpy(), v.double().numpy(), [0, n, 0])
     assert cache.error() == 3
     _check_values(lrkv, cache, oc)
+
+
+def _bound(oc, q, n, G, kept=None):
+    """Reference, and the bound of every element of attention, of the queries
+    q [Hq, n, 128] of the first sequence, which see the tokens `kept` (a mask;
+    default all) up to their own places.
+
+    u = 2^-24, w = sum p |v|, as in test_gpu_quant.py:
+      2^-8 |ref| + w (2^-11 + 2 L u + 2 ds + 2^-20): o's rounding, a rounding of
+      each weight to fp16, the fp32 sums, the scores' errors ds = 128 * 2^-23 *
+      scale * sum |q k| + 2^-21 |score|, the roundings of rescaling.
+    To fp16's floor, 2^-24 a step, half of it a rounding (calls of 17 rows and more;
+    those below have a lower one):
+      weights are held times 2^8 / 2^M' with 2^M' <= max p s, s = the block's scale
+      or, of an open token, 2^-7 of the power of two at or under its row's
+      largest |v|; they meet codes of at most 448 or 2^8 s: 2^-33 of
+      max (p s) * 2^9 each, and max (p s) <= max (p t) 2^-6 with t = the
+      largest |v| of the block (code 127 stands for it), or of the open row:
+      L 2^-30 max (p t) in all;
+      an open row's values are held with the largest in [2^7, 2^8): half a
+      step is 2^-32 of the row's largest: 2^-32 sum (p t);
+      an open row's keys, and q, with the largest in [2^14, 2^15): half a step
+      is 2^-39 of the row's largest, in each of 128 products, on either side: ds
+      grows by 128 * 2^-38 * scale * max |q| max |k of the row|.
+    Nothing in it goes by tokens that the query does not see."""
+    L, H = oc.length(0), oc.H
+    ref, tol = np.zeros((H * G, n, 128)), np.zeros((H * G, n, 128))
+    kept = np.ones(L, bool) if kept is None else kept
+    full = L // 64 * 64
+    for g in range(H * G):
+        K, V = oc.values(0, g // G, 0), oc.values(0, g // G, 1)
+        top = np.abs(V).max(1)
+        for j in range(0, full, 64):
+            top[j:j + 64] = top[j:j + 64].max()
+        for i in range(n):
+            at = np.flatnonzero(kept[:L - n + i + 1])
+            if not len(at):
+                continue
+            k, v, t = K[at], V[at], top[at]
+            s = k @ q[g, i] * SCALE
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            ds = (128 * 2.0 ** -23 * (np.abs(k) @ np.abs(q[g, i])).max() * SCALE
+                  + 2.0 ** -21 * np.abs(s).max()
+                  + 128 * 2.0 ** -38 * SCALE * np.abs(q[g, i]).max() * np.abs(k).max())
+            ref[g, i], w = p @ v, p @ np.abs(v)
+            tol[g, i] = 2.0 ** -8 * np.abs(ref[g, i]) + w * (2.0 ** -11 + 2 * L * 2.0 ** -24 + 2 * ds
+                                                             + 2.0 ** -20)
+            tol[g, i] += L * 2.0 ** -30 * (p * t).max() + 2.0 ** -32 * (p * t).sum()
+    return ref, tol
+
+
+def _attend(lrkv, cache, q):
+    o = torch.full(q.shape, 3.0, dtype=torch.bfloat16, device="cuda")
+    lrkv.quant_attn(cache, q.cuda(), SCALE, o, lrkv.quant_attn_workspace(cache, q.shape[1], q.shape[2]))
+    return o.double().cpu().numpy()
+
+
+# rows per KV head: each kernel and each count of copies of its rows
+CALLS = [(4, 2), (4, 4), (1, 24), (2, 24), (4, 24), (4, 60)]
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("side", [0, 1])
+@pytest.mark.parametrize("G,n", CALLS)
+def test_open_tokens_far_larger_than_earlier_ones(lrkv, code, side, G, n):
+    """A token that a query does not see changes nothing for it, however large
+    its keys or values are; nor does one that it sees take bits from others."""
+    H, L = 2, 64 + 45
+    for gain in (2.0 ** 12, 2.0 ** 40, 2.0 ** 100):
+        x = [_rows(1, 1, H, L), _rows(2, 1, H, L)]
+        x[side][0, :, L - 2] *= gain
+        x[side][0, 1, L - 1] *= 1 / gain
+        cache = lrkv.QuantCache(1, H, L, code=code)
+        oc = qo.QuantCacheOracle(1, H, code)
+        _write(cache, oc, lrkv, *x)
+        q = _rows(3, 1, H * G, n, 0.0)
+        got = _attend(lrkv, cache, q)[0]
+        ref, tol = _bound(oc, q[0].double().numpy(), n, G)
+        # the last two see the large one: where its keys are large, as one that takes all
+        # or nothing
+        err = np.abs(got - ref)
+        assert np.isfinite(got).all()
+        assert (err <= tol)[:, :n - 2].all(), (gain, np.max((err / tol)[:, :n - 2]))
+        if side:
+            assert (err <= tol)[:, n - 2:].all(), (gain, np.max((err / tol)[:, n - 2:]))
+        # the same bits as without the token
+        cut = lrkv.QuantCache(1, H, L, code=code)
+        x[side][0, :, L - 2:] = 1
+        _write(cut, qo.QuantCacheOracle(1, H, code), lrkv, *x)
+        assert np.array_equal(_attend(lrkv, cut, q)[0][:, :n - 2], got[:, :n - 2])
+    assert cache.error() == 0
