@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
           }
           x0 = fmaxf(x0, x1);
         }
-        const float mn = x0 == -INFINITY ? x0 : x0 * f;  // f >= 0
+        const float mn = x0 == -INFINITY ? x0 : x0 * fabsf(f);
         const float vn = mn + ev;
         if (mn > m + kLazy) {  // also from -inf
           l *= ex2_approx(m - mn);
@@ -337,6 +337,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
         if (__any_sync(0xffffffffu, grow)) {
           const float cr = grow ? ex2_approx(mv - vn) : 1.f;
           if (grow) mv = vn;
+          if (__any_sync(0xffffffffu, fabsf(or_zero(mv)) > kWideRef)) fcol = -fabsf(fcol);
           if (k > 0 && quant_wait_warp(&odone[gr], (ns + k - 1) & 1, fail, lane)) {
             tc_fence_after();
 #pragma unroll 1
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
           }
         }
         const float ref = or_zero(m), vref = or_zero(mv);
-        const float wm = fv * ex2_approx(fminf(ref + ev - vref, 112.f) + kBoostLog);
+        const float wm = fv * ex2_approx(fminf(ref - vref + ev, 112.f) + kBoostLog);
         const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f), nref = make_float2(-ref, -ref);
         float2 sum = make_float2(0.f, 0.f);
         auto weigh = [&](auto edge_c) {
@@ -376,7 +377,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
             tmem_st8(tP + copy * (CW / 2) + 8 * q4, pk);
           }
         };
-        if (edge) weigh(std::true_type()); else weigh(std::false_type());
+        if (fcol < 0.f)
+          sum.x = weigh_wide(tS, tP + copy * (CW / 2), CW, fabsf(f), !edge ? CW : sc.ok ? pos - base : -1, ref,
+                             ref - vref + ev + kBoostLog, fv);
+        else if (edge)
+          weigh(std::true_type());
+        else
+          weigh(std::false_type());
         l += sum.x + sum.y;
         tmem_wait_st();
         tc_fence_before();
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
         tc_fence_after();
         if (gr == 1 && nfull == 0) fcol = fc[row];
         const RowState st = open_step({m, l, mv}, tS, tP + copy * (CW / 2), tO, CW,
-                                      sm + pl.tok + at * kTokBytes + copy * CW * 2, fcol,
+                                      sm + pl.tok + at * kTokBytes + copy * CW * 2, fabsf(fcol),
                                       pos - (p.j0 + i) * kStepKeys - copy * CW,
                                       nfull > 0 ? &odone[gr] : nullptr, (ns + nfull - 1) & 1, fail);
         m = st.m;

@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
             }
             x0 = fmaxf(x0, x1);
           }
-          const float mn = x0 == -INFINITY ? x0 : x0 * f;  // f >= 0
+          const float mn = x0 == -INFINITY ? x0 : x0 * fabsf(f);
           const float vn = mn + ev;
           if (mn > m + kLazy) {  // also from -inf
             l *= ex2_approx(m - mn);
@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           if (__any_sync(0xffffffffu, grow)) {
             const float cr = grow ? ex2_approx(mv - vn) : 1.f;
             if (grow) mv = vn;
+            if (__any_sync(0xffffffffu, fabsf(or_zero(mv)) > kWideRef)) fcol = -fabsf(fcol);
             // the step before has been added; this one waits for P
             if (i > 0 && quant_wait_warp(&odone[gr], (nd + i - 1) & 1, fail, lane)) {
               tc_fence_after();
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           }
           const float ref = or_zero(m), vref = or_zero(mv);
           // 2^(m - M') s_v 2^kBoostLog
-          const float wm = fv * ex2_approx(fminf(ref + ev - vref, 112.f) + kBoostLog);
+          const float wm = fv * ex2_approx(fminf(ref - vref + ev, 112.f) + kBoostLog);
           const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f), nref = make_float2(-ref, -ref);
           float2 sum = make_float2(0.f, 0.f);
           auto weigh = [&](auto edge_c) {
@@ -494,7 +495,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
               tmem_st8(tSb + 8 * q4, pk);
             }
           };
-          if (edge) weigh(std::true_type()); else weigh(std::false_type());
+          if (fcol < 0.f)
+            sum.x = weigh_wide(tSb, tSb, kStepKeys, fabsf(f), !edge ? kStepKeys : sc.ok ? pos - base : -1, ref,
+                               ref - vref + ev + kBoostLog, fv);
+          else if (edge)
+            weigh(std::true_type());
+          else
+            weigh(std::false_type());
           l += sum.x + sum.y;
           tmem_wait_st();
           tc_fence_before();
@@ -514,7 +521,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           ns ^= 1u << sb;
           tc_fence_after();
           const RowState r = open_step({m, l, mv}, tSb, tSb, tO, kStepKeys, sm + pl.tok + at * kTokBytes,
-                                       fcol, pos - (p.j0 + nopen) * kStepKeys,
+                                       fabsf(fcol), pos - (p.j0 + nopen) * kStepKeys,
                                        nopen > 0 ? &odone[gr] : nullptr, (nd + nopen - 1) & 1, fail);
           m = r.m;
           l = r.l;

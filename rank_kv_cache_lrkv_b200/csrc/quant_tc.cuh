@@ -240,10 +240,43 @@ static __device__ __noinline__ void open_values(const __nv_bfloat16* rows, int n
   }
 }
 
-// ---- the softmax of the open block
+// ---- the softmax of the open block, and of a step whose exponents are far apart
 //
-// A real function over S in TMEM: it is called once a part, in line it spills.
+// The usual step weighs with v = 2^(s f - m) and v (2^(m - M') s_v 2^kBoostLog).
+// That takes one thing, and a step that lacks it is weighed by weigh_wide
+// (a real function over S in TMEM: it is seldom called):
+//  * |m| small: m is s f rounded and s f in the fma is not, so v is off by 2 to half
+//    an ulp of m, alike for all tokens of a row; from 2^24 on a weight could
+//    overflow.  |M'| tells (it moves with m) and is looked at where it moves; a warp
+//    with such a row has its factors fcol negated for the rest of the part.  (What multiplies v takes m - M' first:
+//    that is exact.)
+constexpr float kWideRef = 1048576.f;
 __device__ __forceinline__ float or_zero(float x) { return x == -INFINITY ? 0.f : x; }
+// Weights of the columns of S up to `last` (0 behind it) to TMEM at tP, which may be
+// where S is; returns their sum.  c: log2 of what p is multiplied by, beside fv.
+static __device__ __noinline__ float weigh_wide(uint32_t tS, uint32_t tP, int columns, float f, int last,
+                                                float ref, float c, float fv) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int k0 = 0; k0 < columns; k0 += 16) {
+    uint32_t s[16], pk[8];
+    tmem_ld16(tS + k0, s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float w[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float x = __fmul_rn(__uint_as_float(s[2 * e + u]), f) - ref;
+        const bool out = k0 + 2 * e + u > last;
+        sum += out ? 0.f : ex2_approx(x);
+        w[u] = out ? 0.f : fv * ex2_approx(x + c);
+      }
+      pk[e] = pack_h2(w[0], w[1]);
+    }
+    tmem_st8(tP + (k0 >> 1), pk);
+  }
+  return sum;
+}
 // A row's state, and the open block's step: the columns of S up to `last`, P, O
 // (whose last sums `odone` tells of; nullptr: there are none yet).  tok: the
 // columns' tokens, fcol: the row's factor.

@@ -165,3 +165,41 @@ def test_open_tokens_far_larger_than_earlier_ones(lrkv, code, side, G, n):
         _write(cut, qo.QuantCacheOracle(1, H, code), lrkv, *x)
         assert np.array_equal(_attend(lrkv, cut, q)[0][:, :n - 2], got[:, :n - 2])
     assert cache.error() == 0
+
+
+def _along(c, n, gain):
+    """Keys c_t u and queries u for u of +-1: scores 128 c_t gain SCALE."""
+    u = np.sign(np.random.default_rng(1).standard_normal(128))
+    k = torch.from_numpy((c[:, None] * u).astype(np.float32)).to(torch.bfloat16)
+    q = torch.from_numpy(np.tile(u * gain, (n, 1)).astype(np.float32)).to(torch.bfloat16)
+    assert np.array_equal(k.double().numpy(), c[:, None] * u)
+    return k, q
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,n", CALLS)
+def test_scores_of_millions(lrkv, code, G, n):
+    """Scores far above those at which fp32 tells two tokens from each other: the
+    largest takes all, and the result is its value."""
+    L = 150
+    v = _rows(2, 1, 1, L)
+    for sign in (1, -1):
+        # a query's largest score is that of the last of these that it sees
+        c = np.full(L, 0.5 if sign > 0 else -2.0)
+        c[[0, 100, 140]] = [1, 2, 4] if sign > 0 else [-1, -0.5, -0.25]
+        for gain in (2.0 ** 8, 2.0 ** 22, 2.0 ** 25, 2.0 ** 40, 2.0 ** 100):
+            k, q = _along(c, n, gain)
+            cache = lrkv.QuantCache(1, 1, L, code=code)
+            oc = qo.QuantCacheOracle(1, 1, code)
+            _write(cache, oc, lrkv, k[None, None], v)
+            got = _attend(lrkv, cache, q[None, None].expand(1, G, n, 128).contiguous())[0]
+            K, V = oc.values(0, 0, 0), oc.values(0, 0, 1)
+            for i in range(n):
+                pos = L - n + i
+                s = np.sort(K[:pos + 1] @ q[i].double().numpy() * SCALE)
+                # nothing of any other token is left: 2 ds (see _bound) away and more
+                assert s[-1] - s[-2] > 2 * (128 * 2.0 ** -23 + 2.0 ** -21) * np.abs(s).max() + 200
+                want = V[140 if pos >= 140 else 100 if pos >= 100 else 0]
+                # o's rounding, the weight's, and the few of a sum of one term
+                tol = np.abs(want) * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20)
+                assert (np.abs(got[:, i] - want) <= tol).all(), (sign, gain, i)
