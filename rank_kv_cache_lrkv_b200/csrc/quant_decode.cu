@@ -439,17 +439,17 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
                     mx = fmaxf(mx, v);
                   }
                 mx = col_max(mx);
-                const float mvn = fmaxf(mv[2 * n + j], mx + ev);
-                mx = fmaxf(mx, m[2 * n + j]);
-                const float ref = mx == -INFINITY ? 0.f : mx;
+                const float mvn = fmaxf(mv[2 * n + j], mx + ev), mn = fmaxf(mx, m[2 * n + j]);
+                const float ref = mn == -INFINITY ? 0.f : mn, bref = mx == -INFINITY ? 0.f : mx;
                 const float vref = mvn == -INFINITY ? 0.f : mvn;
-                const float cr = ex2_approx(m[2 * n + j] - ref);
+                const float cr = ex2_approx(m[2 * n + j] - ref), cb = ex2_approx(mx - ref);
                 moved |= mvn != mv[2 * n + j];
                 corr[2 * n + j] = ex2_approx(mv[2 * n + j] - vref);
-                m[2 * n + j] = mx;
+                m[2 * n + j] = mn;
                 mv[2 * n + j] = mvn;
-                // 2^(m - M') s_v 2^13 (no more than 2^126: p is 0 there)
-                const float wmul = fv * ex2_approx(fminf(ref + ev - vref, 112.f) + 13.f);
+                // p by the block's own maximum, so that one that counts for its
+                // values is not flushed; then 2^(maximum - M') s_v 2^13, at most 2^14
+                const float wmul = fv * ex2_approx(mx - vref + ev + 13.f);
                 float sum = 0.f;
 #pragma unroll
                 for (int s4 = 0; s4 < 4; ++s4)
@@ -457,11 +457,11 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
                   for (int u = 0; u < 2; ++u) {
                     float& v = sacc[s4][n][2 * u + j];
                     const bool out = edge && v == -INFINITY;
-                    v = ex2_approx(v - ref);
+                    v = ex2_approx(v - bref);
                     sum += v;
                     v = out ? 0.f : v * wmul;  // a NaN scale does not reach what is masked
                   }
-                l[2 * n + j] = l[2 * n + j] * cr + sum;
+                l[2 * n + j] = l[2 * n + j] * cr + sum * cb;
               }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll

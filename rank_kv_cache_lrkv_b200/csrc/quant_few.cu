@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
           }
         }
         const float ref = or_zero(m), vref = or_zero(mv);
-        const float wm = fv * ex2_approx(fminf(ref - vref + ev, 112.f) + kBoostLog);
+        const float wm = fv * ex2_approx(ref - vref + ev + kBoostLog);
         const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f), nref = make_float2(-ref, -ref);
         float2 sum = make_float2(0.f, 0.f);
         auto weigh = [&](auto edge_c) {
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
             tmem_st8(tP + copy * (CW / 2) + 8 * q4, pk);
           }
         };
-        if (fcol < 0.f)
+        if (fcol < 0.f || sc.ok == kWideStep)
           sum.x = weigh_wide(tS, tP + copy * (CW / 2), CW, fabsf(f), !edge ? CW : sc.ok ? pos - base : -1, ref,
                              ref - vref + ev + kBoostLog, fv);
         else if (edge)
@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
     bool live = true;
     for (int x = lo; x < hi && live; advance(p, x)) {
       const int L = slen[p.b];
+      bool low = false;
       auto written = [&]() {
         fence_proxy_async_smem();
         mbar_arrive(&tfull[buf]);
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
           StepScales* s = &scales[cnt % kFewScales];
           s->sk = sk;
           s->sv = sv;
-          s->ok = there ? 1 : 0;
+          s->ok = there ? wide_step(sv, low) : 0;
         }
         written();
       }

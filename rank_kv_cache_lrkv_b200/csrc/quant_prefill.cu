@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           }
           const float ref = or_zero(m), vref = or_zero(mv);
           // 2^(m - M') s_v 2^kBoostLog
-          const float wm = fv * ex2_approx(fminf(ref - vref + ev, 112.f) + kBoostLog);
+          const float wm = fv * ex2_approx(ref - vref + ev + kBoostLog);
           const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f), nref = make_float2(-ref, -ref);
           float2 sum = make_float2(0.f, 0.f);
           auto weigh = [&](auto edge_c) {
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
               tmem_st8(tSb + 8 * q4, pk);
             }
           };
-          if (fcol < 0.f)
+          if (fcol < 0.f || sc.ok == kWideStep)
             sum.x = weigh_wide(tSb, tSb, kStepKeys, fabsf(f), !edge ? kStepKeys : sc.ok ? pos - base : -1, ref,
                                ref - vref + ev + kBoostLog, fv);
           else if (edge)
@@ -668,6 +668,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
     for (long long x = lo; x < hi && live; advance(p, x)) {
       const int L = slen[p.b], last = max(p.nt0, p.nt1);
       const int j1 = min(p.j1, last), jf = min(j1, L / kQBlock);  // full blocks; then the open one
+      bool low = false;
       if (p.j0 < jf) {
         page(p, p.j0, entry(p, p.j0));
         load_k();
@@ -709,7 +710,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           StepScales* s = &scales[cnt % kScaleRing];
           s->sk = sk;
           s->sv = sv;
-          s->ok = there ? 1 : 0;
+          s->ok = there ? wide_step(sv, low) : 0;
         }
         fence_proxy_async_smem();
         __syncwarp();

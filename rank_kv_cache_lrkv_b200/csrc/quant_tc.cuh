@@ -18,7 +18,7 @@ constexpr float kBoostLog = 8.f;
 
 struct alignas(16) StepScales {
   float sk, sv;
-  int ok;       // the page's tokens count
+  int ok;       // the page's tokens count (kWideStep: weighed by weigh_wide)
 };
 // The open block's tokens have powers of two of their own (so that no token takes
 // bits from others, least of all from those of queries that do not see it): the
@@ -243,14 +243,26 @@ static __device__ __noinline__ void open_values(const __nv_bfloat16* rows, int n
 // ---- the softmax of the open block, and of a step whose exponents are far apart
 //
 // The usual step weighs with v = 2^(s f - m) and v (2^(m - M') s_v 2^kBoostLog).
-// That takes one thing, and a step that lacks it is weighed by weigh_wide
+// That takes two things, and a step that lacks either is weighed by weigh_wide
 // (a real function over S in TMEM: it is seldom called):
+//  * 2^(m - M') s_v small, as v is flushed under 2^-126.  M' is at most kLazy under m +
+//    log2 of the value scale where m was found, so with all scales of a part in
+//    [2^-35, 2^35] the factor is at most 2^(70 + kLazy + 1 + kBoostLog), and weights
+//    under 2^-41 are flushed (half of fp16's smallest step is 2^-25).  The
+//    converters mark a step whose scale is above that range, or whose part had one
+//    below it (wide_step).
 //  * |m| small: m is s f rounded and s f in the fma is not, so v is off by 2 to half
 //    an ulp of m, alike for all tokens of a row; from 2^24 on a weight could
 //    overflow.  |M'| tells (it moves with m) and is looked at where it moves; a warp
 //    with such a row has its factors fcol negated for the rest of the part.  (What multiplies v takes m - M' first:
 //    that is exact.)
+constexpr int kWideStep = 2;
 constexpr float kWideRef = 1048576.f;
+// StepScales::ok of a full block; low: it, or a block of its part before it, was under the range.
+__device__ __forceinline__ int wide_step(float sv, bool& low) {
+  low |= sv < 2.9103830456733704e-11f;               // 2^-35
+  return low || sv > 34359738368.f ? kWideStep : 1;  // 2^35
+}
 __device__ __forceinline__ float or_zero(float x) { return x == -INFINITY ? 0.f : x; }
 // Weights of the columns of S up to `last` (0 behind it) to TMEM at tP, which may be
 // where S is; returns their sum.  c: log2 of what p is multiplied by, beside fv.

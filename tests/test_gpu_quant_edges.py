@@ -203,3 +203,52 @@ def test_scores_of_millions(lrkv, code, G, n):
                 # o's rounding, the weight's, and the few of a sum of one term
                 tol = np.abs(want) * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20)
                 assert (np.abs(got[:, i] - want) <= tol).all(), (sign, gain, i)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,n", CALLS)
+@pytest.mark.parametrize("big", [0, 70, 140])
+def test_values_far_apart(lrkv, code, G, n, big):
+    """A block of next to no weight with a token whose values are so much larger that
+    it counts: weights of 2^-125 and more of the largest are kept whatever the values
+    are."""
+    L = 150
+    for low, high, weight in ((-60, 60, 118), (-60, 60, 124), (-100, 20, 121), (0, 85, 90)):
+        at = slice(big // 64 * 64, big // 64 * 64 + 64)
+        c = np.zeros(L)
+        c[at] = -1
+        gain = weight * np.log(2) / (128 * SCALE)
+        k, q = _along(c, n, gain)
+        v = _rows(2, 1, 1, L, 0.0) * 2.0 ** low
+        v[:, :, at] *= 2.0 ** -10
+        v[:, :, big] = _rows(3, 1, 1, 1, 0.0)[:, :, 0] * 2.0 ** high
+        cache = lrkv.QuantCache(1, 1, L, code=code)
+        oc = qo.QuantCacheOracle(1, 1, code)
+        _write(cache, oc, lrkv, k[None, None], v)
+        q = q[None, None].expand(1, G, n, 128).contiguous()
+        got = _attend(lrkv, cache, q)[0]
+        ref, tol = _bound(oc, q[0].double().numpy(), n, G)
+        assert (np.abs(got - ref) <= tol).all(), (low, high, weight, np.max(np.abs(got - ref) / tol))
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,n", [(4, 1), (4, 4), (4, 8)])
+def test_values_far_apart_in_long_parts(lrkv, code, G, n):
+    """The same where one CTA takes all blocks of a sequence, several to a warp."""
+    B, L = 200, 15 * 64 + 10
+    for big, (low, high, weight) in ((0, (-60, 60, 118)), (100, (-60, 60, 124)), (600, (-100, 20, 121)),
+                                     (900, (0, 85, 90)), (900, (-60, 60, 118))):
+        at = slice(big // 64 * 64, big // 64 * 64 + 64)
+        c = np.zeros(L)
+        c[at] = -1
+        k, q = _along(c, n, weight * np.log(2) / (128 * SCALE))
+        v = _rows(2, 1, 1, L, 0.0) * 2.0 ** low
+        v[:, :, big] = _rows(3, 1, 1, 1, 0.0)[:, :, 0] * 2.0 ** high
+        oc = qo.QuantCacheOracle(1, 1, code)
+        oc.append(k[None, None].double().numpy(), v.double().numpy())
+        cache = lrkv.QuantCache(B, 1, L, code=code)
+        lrkv.quant_append(cache, *(x.expand(B, 1, L, 128).contiguous().cuda() for x in (k, v)))
+        q = q.expand(B, G, n, 128).contiguous()
+        got = _attend(lrkv, cache, q)
+        ref, tol = _bound(oc, q[0].double().numpy(), n, G)
+        assert (np.abs(got - ref) <= tol).all(), (big, low, high, weight, np.max(np.abs(got - ref) / tol))
