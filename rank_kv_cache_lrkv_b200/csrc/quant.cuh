@@ -122,6 +122,15 @@ __device__ __forceinline__ bool quant_wait_warp(uint64_t* bar, uint32_t parity, 
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// The slabs last asked for, one a stage of the ring, have landed (or two seconds
+// passed): a CTA does not end before its copies, whoever gave up on one.
+__device__ __forceinline__ void quant_drain(uint64_t* bars, int issued, int stages) {
+  const uint64_t t0 = global_ns();
+  for (int k = max(0, issued - stages); k < issued; ++k)
+    while (!mbar_try_wait(&bars[k % stages], (k / stages) & 1) && global_ns() - t0 < 2000000000ull) {
+    }
+}
+
 // Launch arguments of the append, read and attention kernels.
 struct QuantAppendArgs {
   QuantView c;

@@ -763,15 +763,9 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
     x = p.first + p.i1;
     if (x < hi) next_part(p);
   }
-  if (*fail) {
-    // copies still landing end before the CTA does
-    if (warp < W && lane == 0) {
-      const uint64_t t0 = global_ns();
-      for (int k = n_read; k < n_issued; ++k)
-        while (!mbar_try_wait(&bar[k % D], (k / D) & 1) && global_ns() - t0 < kTcTimeoutNs) {
-        }
-      quant_error(c, kErrTimeout);
-    }
+  if (*fail && warp < W && lane == 0) {
+    quant_drain(bar, n_issued, D);
+    quant_error(c, kErrTimeout);
   }
 }
 

@@ -688,15 +688,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
         }
       }
     }
-    if (!live || *fail) {
-      // copies still landing end before the CTA does
-      if (lane == 0) {
-        const uint64_t t0 = global_ns();
-        for (int k = max(0, issued - NR); k < issued; ++k)
-          while (!mbar_try_wait(&rawfull[k % NR], (k / NR) & 1) && global_ns() - t0 < kTcTimeoutNs) {
-          }
-      }
-    }
+    if (lane == 0) quant_drain(rawfull, issued, NR);
   }
   tc_fence_before();
   __syncthreads();

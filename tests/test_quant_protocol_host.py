@@ -27,3 +27,23 @@ def test_an_append_counts_a_cta_after_all_its_warps_have_read_the_length():
     head, tail = before.rsplit("__syncthreads();", 1)
     assert re.fullmatch(r" if \(tid == 0\) \{ __threadfence\(\); const int last = [^;{}]*; if \(", tail)
     assert head.count("{") - head.count("}") == 1
+
+
+def test_copies_still_landing_when_a_wait_gave_up_are_waited_for():
+    """A CTA may not end with a bulk copy into its shared memory under way.  A
+    warp that gives up on a page goes on counting it as read, so what may still
+    land are the last slabs asked for, one a stage, read or not; and a role that
+    ended well cannot know that another gives up later."""
+    helper = _source("quant.cuh")
+    body = helper[helper.index("void quant_drain("):]
+    assert body.startswith("void quant_drain(uint64_t* bars, int issued, int stages) { "
+                           "const uint64_t t0 = global_ns(); "
+                           "for (int k = max(0, issued - stages); k < issued; ++k) "
+                           "while (!mbar_try_wait(&bars[k % stages], (k / stages) & 1) && "
+                           "global_ns() - t0 < ")
+    decode, few = _source("quant_decode.cu"), _source("quant_few.cu")
+    # a failed wait sets `fail` for the warp that looks at its own slabs here
+    assert "if (*fail && warp < W && lane == 0) { quant_drain(bar, n_issued, D);" in decode
+    assert re.search(r"\} \} \} \} if \(lane == 0\) quant_drain\(rawfull, issued, NR\); \}", few)
+    for text in (decode, few):
+        assert text.count("quant_drain(") == 1
