@@ -448,8 +448,12 @@ int lrkv_quant_read(const lrkv_quant_cache *cache, const int32_t *first, int32_t
  *          batch * num_kv_heads * (max_pages_per_seq + 16) and, with R =
  *          n_queries * that ratio, ceil(R / 256) * (max_pages_per_seq + 16)
  *          must fit 31 bits, R 30 (LRKV_ERR_UNSUPPORTED otherwise).
- *   A key or value that is not finite makes NaN of the queries that see it
- *          (a full block's of those that see the block) and of no others.
+ *   A NaN, an open token's value that is not finite, and a full block holding
+ *          anything that is not finite make NaN of the queries that see them
+ *          (the token, or a token of the block) and of no others.  An infinity
+ *          among an open token's keys is the score that it gives: +inf makes NaN,
+ *          with -inf the token has no weight; a query of whose tokens none has any
+ *          gets o = 0.
  *   workspace : at least lrkv_quant_attn_workspace_bytes, 16-byte aligned,
  *          zeroed when allocated (the calls leave their counters at zero);
  *          calls sharing a workspace must be stream-ordered. */

@@ -252,3 +252,43 @@ def test_values_far_apart_in_long_parts(lrkv, code, G, n):
         got = _attend(lrkv, cache, q)
         ref, tol = _bound(oc, q[0].double().numpy(), n, G)
         assert (np.abs(got - ref) <= tol).all(), (big, low, high, weight, np.max(np.abs(got - ref) / tol))
+
+
+@pytest.mark.parametrize("G,n", CALLS)
+def test_infinite_keys_of_the_open_block(lrkv, G, n):
+    """An infinity among an open token's keys is the score that the formula has: of
+    -inf its weight is 0, as if it were not there, +inf makes NaN.  In a full
+    block it makes NaN either way."""
+    H, L, at = 1, 64 + 45, 100
+    x = [_rows(1, 1, H, L), _rows(2, 1, H, L)]
+    oc = qo.QuantCacheOracle(1, H, "int8")
+    oc.append(*(y.double().numpy() for y in x))
+    x[0][0, 0, at, 7] = float("inf")
+    cache = lrkv.QuantCache(1, H, 128)
+    lrkv.quant_append(cache, *(y.cuda() for y in x))
+    q = _rows(3, 1, H * G, n, 0.0)
+    sign = torch.ones(G, n)
+    sign.view(-1)[::3] = -1
+    q[0, :, :, 7] = sign.to(torch.bfloat16)
+    got = _attend(lrkv, cache, q)[0]
+    kept = np.arange(L) != at
+    ref, tol = _bound(oc, q[0].double().numpy(), n, G, kept)
+    sees = (L - n + np.arange(n) >= at)[None] & (sign.numpy() > 0)
+    assert np.isnan(got).all(-1)[sees].all()
+    assert (np.abs(got - ref) <= tol)[~sees].all()
+    # the block becomes full
+    lrkv.quant_append(cache, *(_rows(5, 1, H, 19).cuda() for _ in range(2)))
+    assert np.isnan(_attend(lrkv, cache, q)[0]).all()
+
+
+@pytest.mark.parametrize("G,n", CALLS)
+def test_scores_of_minus_infinity_alone(lrkv, G, n):
+    """A query of whose tokens none counts gets 0."""
+    k, v = _rows(1, 1, 1, 3), _rows(2, 1, 1, 3)
+    k[..., 7] = float("-inf")
+    cache = lrkv.QuantCache(1, 1, 64)
+    lrkv.quant_append(cache, k.cuda(), v.cuda())
+    q = _rows(3, 1, G, n, 0.0)
+    q[..., 7] = 2
+    assert not _attend(lrkv, cache, q).any()
+    assert cache.error() == 0
