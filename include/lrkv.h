@@ -454,6 +454,12 @@ int lrkv_quant_read(const lrkv_quant_cache *cache, const int32_t *first, int32_t
  *          among an open token's keys is the score that it gives: +inf makes NaN,
  *          with -inf the token has no weight; a query of whose tokens none has any
  *          gets o = 0.
+ *   Roundings: a weight to fp16 once, o to bf16 once; maxima and sums in fp32.
+ *          fp16 has a floor: a weight times its value of 2^-30 of the query's
+ *          largest and less may count for nothing.  q, and where R is above 16
+ *          the open tokens' keys and values, are fp16 under a power of two for
+ *          each row of 128: what is under 2^-31 (values 2^-24) of its row's
+ *          largest loses bits.
  *   workspace : at least lrkv_quant_attn_workspace_bytes, 16-byte aligned,
  *          zeroed when allocated (the calls leave their counters at zero);
  *          calls sharing a workspace must be stream-ordered. */

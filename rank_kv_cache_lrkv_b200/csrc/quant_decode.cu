@@ -3,20 +3,26 @@
 // Row r of a unit (sequence, KV head) is query r / G of q head h G + r % G.
 // A code is an exact fp16 number, so with q brought to fp16 (exactly: times
 // a power of two that puts its row's largest element in [2^14, 2^15); what
-// is 2^-28 of that and less loses bits) and the block's scales kept outside,
+// is under 2^-31 of that loses bits) and the block's scales kept outside,
 //   score = (q . c_k) (s_k scale 2^e),  acc += (p s_v) c_v
 // run on mma.sync m16n8k16 with fp32 accumulation.  Besides the softmax's
 // running maximum m a row keeps M', the running maximum of a block's largest
 // score + floor(log2 s_v): the weights 2^(score - M') s_v 2^13 are then at
 // most 2^14 whatever the blocks' scales, are rounded to fp16 once and keep
-// eleven bits down to 2^-27 of the largest.
+// eleven bits down to 2^-27 of the largest.  Within a block p goes by the block's
+// own maximum.
 //
-// What bounds it: HBM for long caches (64 sequences of 12,288 tokens on
-// average x 8 heads: 1.6 GB in 274 us, 5,900 GB/s; 4 of 32,769: 47 us, 5,770),
-// latency for short ones: 7 to 8 us between the launch and the last part
-// folded (512 tokens 8.2 us, 4 x 8192 17.3 us).  With 9 to 16 rows a page's
-// exponentials and products take a warp longer than its bytes take to arrive:
-// 8 sequences of 12,288, 16 rows, 55 us (3,900 GB/s).
+// What bounds it (calls over several caches in turn, more than L2 holds, at the
+// clock named): HBM for long caches (64 sequences of 12,288 tokens x 8 heads: 1.6 GB
+// in 246 us at 1,965 MHz, 286 in a long run at 1,700; 4 of 32,769: 50 us, 5,390 GB/s
+// at 1,940), latency for short ones: 8 to 9 us between the launch and the last part
+// folded (512 tokens 8.5 us, 4 x 8192 19.8 us, both at 1,965 MHz).  With 9 to 16 rows
+// no pipe is full (issue slots 34 %, warp MMAs 18 %, DRAM 39 %): a warp's only slab is
+// empty while its next page comes, and its page takes it a chain of products,
+// exponentials and products.  8 sequences of 12,288, 16 rows: 56 us int8, 52 e4m3
+// (3,580 and 3,860 GB/s, 1,965 MHz).
+// Figures of one choice against another, below, are of calls back to back on one
+// cache, of which L2 keeps a part.
 //
 // One launch, persistent, one CTA per SM.  The blocks of all units are laid
 // end to end and each CTA takes an equal contiguous range (the caller keeps
@@ -800,8 +806,8 @@ int quant_attn_launch(const QuantAttnArgs& a, cudaStream_t st) {
   const int rc = current_device_info(dev, info);
   if (rc != LRKV_OK) return rc;
   // Six consumer warps with two slabs each: one token of the 32K layer (G 4)
-  // 51.7 us, 64 sequences of 12000 239 us (6,576 GB/s); five warps 58.0 and
-  // 269, eight with one slab each 57.1 and 261, four with three 53.9 and 254.
+  // 51.7 us, 64 sequences of 12000 239 us; five warps 58.0 and 269, eight with one
+  // slab each 57.1 and 261, four with three 53.9 and 254 (this kernel's first form).
   // More sequences than the lengths' place in shared memory allows: five.
   if ((long long)a.n * a.G <= 8) {
     if (dec_plan(6, 2, 8, a.c.B).total <= info.optin)
@@ -813,11 +819,12 @@ int quant_attn_launch(const QuantAttnArgs& a, cudaStream_t st) {
   // eight of one, which spills, 67.5; the tensor-memory kernel 97).
   if ((long long)a.n * a.G <= kMaxRows)
     return a.c.e4m3 ? launch<true, 2, 7, 1>(a, info, st) : launch<false, 2, 7, 1>(a, info, st);
-  // Up to a tile's rows in copies over the tile, against quant_prefill.cu: 4 x
-  // 16384 tokens with 20, 64 and 128 rows 55, 61 and 82 us against 82, 84 and
-  // 88; 64 x 512 with 32, 64 and 128: 56, 62 and 83 against 80, 80 and 80.
-  // (Where a CTA has one short unit 128 rows lose, 16 x 1024 tokens 46 us
-  // against 38: lengths are on the device, so no rule here can tell.)
+  // Up to a tile's rows in copies over the tile, against quant_prefill.cu (caches
+  // in turn, 1,965 MHz): 4 x 16384 tokens with 20, 64 and 128 rows 53, 58 and 78 us
+  // against 80, 82 and 86; 64 x 512 with 32, 64 and 128: 56, 62 and 87 against 72, 72
+  // and 73.  (Where a CTA has short units 128 rows lose, 16 x 1024 tokens 46 us
+  // against 39.  Lengths are on the device; max_pages_per_seq, a bound on them, is
+  // not used for a rule.)
   if ((long long)a.n * a.G <= 128) return quant_few_launch(a, info, st);
   return quant_prefill_launch(a, info, st);
 }

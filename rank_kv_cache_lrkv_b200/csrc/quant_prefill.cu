@@ -25,10 +25,10 @@
 // is the chain of a step through softmax (2000: TMEM's latency, the row
 // maximum, the exponentials, the hand-over) and back through the products.  And
 // the card: in a long run it draws 990 W, its limit, at 1.78 GHz of 1.965.
-// 2048 queries of 32 heads over 2 x 16,384 tokens: 1.04 ms (990 TFLOP/s) on a
-// cool card, 1.15 ms (895) in a long run; 8192 over themselves 0.60 to 0.65 ms
-// (910 to 855).  A tile's start and end take 12 to 16 thousand clocks: 32
-// prompts of 512 tokens 200 us (340 TFLOP/s).
+// 2048 queries of 32 heads over 2 x 16,384 tokens: 1.05 ms (990 TFLOP/s) on a
+// cool card at 1,965 MHz, 1.16 ms (885) in a long run at 1,800; 8192 over themselves
+// 0.61 to 0.65 ms (905 to 850).  A tile's start and end take 12 to 16 thousand
+// clocks: 32 prompts of 512 tokens 198 us (347 TFLOP/s, 1,965 MHz).
 // Measured against it, the 2048 queries: two threads a row on sixteen softmax
 // warps 1.38 ms against 1.09 (what a row costs once is paid twice); sixteen
 // warps that take a row's steps in turns 1.17 against 1.12; one S that is given
@@ -66,8 +66,8 @@ constexpr int kScaleRing = 8;
 // few tiles share a page: 0.39 ms without, 0.33 with; 2, 3 and 4 alike).
 constexpr int kFar = 3;
 // A tile's start and end (its rows of q and o, the empty pipeline) take about
-// as long as this many steps; the ranges count them.  (5, 8, 12: 42 prompts of
-// 189 tokens 65, 62 and 54 us, one of 8192 604, 610 and 626.)
+// as long as this many steps; the ranges count them.  (5, 8, 12: 168 prompts of
+// 189 tokens 89, 94 and 92 us, one of 8192 on a cool card 601, 608 and 624.)
 constexpr int kTileSteps = 8;
 struct PrePlan {
   int q, k, v, bars, scales, tok, parts, misc, start, len, nq, sum, total;
