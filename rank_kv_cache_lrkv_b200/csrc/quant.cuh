@@ -50,6 +50,7 @@ __host__ __device__ __forceinline__ int quant_k_chunk(int t, int ch) {
   return t * kHeadDim + ((ch ^ ((t & 1) << 2)) << 4);
 }
 
+__device__ __forceinline__ float or_zero(float x) { return x == -INFINITY ? 0.f : x; }
 // a + b on two fp32 lanes at once.
 __device__ __forceinline__ float2 add2(const float2 a, const float2 b) {
   unsigned long long dd, aa, bb;

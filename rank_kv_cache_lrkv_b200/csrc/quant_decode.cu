@@ -8,9 +8,10 @@
 // run on mma.sync m16n8k16 with fp32 accumulation.  Besides the softmax's
 // running maximum m a row keeps M', the running maximum of a block's largest
 // score + floor(log2 s_v): the weights 2^(score - M') s_v 2^13 are then at
-// most 2^14 whatever the blocks' scales, are rounded to fp16 once and keep
+// most 2^15 whatever the blocks' scales, are rounded to fp16 once and keep
 // eleven bits down to 2^-27 of the largest.  Within a block p goes by the block's
-// own maximum.
+// own maximum.  Maxima are held rounded down to whole numbers, M' as what it is
+// above m: both are exact however large the scores are, and so is every rescaling.
 //
 // What bounds it (calls over several caches in turn, more than L2 holds, at the
 // clock named): HBM for long caches (64 sequences of 12,288 tokens x 8 heads: 1.6 GB
@@ -73,7 +74,7 @@ __host__ __device__ inline DecPlan dec_plan(int W, int D, int rows, int B) {
   return p;
 }
 
-// Workspace: a counter per CTA, then two records of [16][132] fp32 (m, l, M',
+// Workspace: a counter per CTA, then two records of [16][132] fp32 (m, l, M' - m,
 // -, 128 sums) per CTA.  Of the units that a CTA shares with others one at
 // most begins in it and one at most began before it: they have record 1 and
 // record 0, and the unit's counter is that of the CTA in which it begins.
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
   const DecPlan pl = dec_plan(W, D, kRows, c.B);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + pl.full);
   float* slots = reinterpret_cast<float*>(sm + pl.slots);
-  float4* ml = reinterpret_cast<float4*>(sm + pl.ml);  // [W + 1][kRows] (m, l, M')
+  float4* ml = reinterpret_cast<float4*>(sm + pl.ml);  // [W + 1][kRows] (m, l, M' - m)
   int* start = reinterpret_cast<int*>(sm + pl.start);
   int* slen = reinterpret_cast<int*>(sm + pl.len);
   int* snq = reinterpret_cast<int*>(sm + pl.nq);
@@ -314,11 +315,11 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
     if (p.i1 <= 0) break;  // the range ends before the unit's first block
     const int L = slen[p.b], nq = snq[p.b], rows = nq * a.G;  // at most kRows
     const int pos0 = L - nq;  // position of query 0
-    float m[2 * NT], l[2 * NT], mv[2 * NT], acc[8][NT][4];
+    float m[2 * NT], l[2 * NT], dv[2 * NT], acc[8][NT][4];
     int pos[2 * NT];
 #pragma unroll
     for (int i = 0; i < 2 * NT; ++i) {
-      m[i] = mv[i] = -INFINITY;
+      m[i] = dv[i] = -INFINITY;
       l[i] = 0.f;
       // this lane's columns: row 8 (i / 2) + 2 t + i % 2
       const int r = 8 * (i >> 1) + 2 * t + (i & 1);
@@ -445,17 +446,20 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
                     mx = fmaxf(mx, v);
                   }
                 mx = col_max(mx);
-                const float mvn = fmaxf(mv[2 * n + j], mx + ev), mn = fmaxf(mx, m[2 * n + j]);
-                const float ref = mn == -INFINITY ? 0.f : mn, bref = mx == -INFINITY ? 0.f : mx;
-                const float vref = mvn == -INFINITY ? 0.f : mvn;
-                const float cr = ex2_approx(m[2 * n + j] - ref), cb = ex2_approx(mx - ref);
-                moved |= mvn != mv[2 * n + j];
-                corr[2 * n + j] = ex2_approx(mv[2 * n + j] - vref);
+                mx = floorf(mx);
+                const float mn = fmaxf(mx, m[2 * n + j]);
+                const float ref = or_zero(mn), bref = or_zero(mx);
+                // from the old maximum and from the block's to the new one
+                const float sh = m[2 * n + j] - ref, bsh = mx - ref;
+                const float cr = ex2_approx(sh), cb = ex2_approx(bsh);
+                const float old = dv[2 * n + j] + sh, dn = fmaxf(old, bsh + ev), dref = or_zero(dn);
+                moved |= dn != old;
+                corr[2 * n + j] = ex2_approx(old - dref);
                 m[2 * n + j] = mn;
-                mv[2 * n + j] = mvn;
+                dv[2 * n + j] = dn;
                 // p by the block's own maximum, so that one that counts for its
-                // values is not flushed; then 2^(maximum - M') s_v 2^13, at most 2^14
-                const float wmul = fv * ex2_approx(mx - vref + ev + 13.f);
+                // values is not flushed; then 2^(maximum - M') s_v 2^13: at most 2^15 in all
+                const float wmul = fv * ex2_approx(bsh + ev - dref + 13.f);
                 float sum = 0.f;
 #pragma unroll
                 for (int s4 = 0; s4 < 4; ++s4)
@@ -564,8 +568,9 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
               mx = fmaxf(mx, v);
             }
           mx = col_max(mx);
-          m[2 * n + j] = mv[2 * n + j] = mx;
-          const float ref = mx == -INFINITY ? 0.f : mx;
+          m[2 * n + j] = mx = floorf(mx);
+          dv[2 * n + j] = 0.f;
+          const float ref = or_zero(mx);
           float sum = 0.f;
 #pragma unroll
           for (int s4 = 0; s4 < 4; ++s4)
@@ -634,7 +639,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
           if (base + bad <= pos[i]) l[i] = NAN;
     }
 
-    // ---------------- combine the warps' (m, l, M', acc)
+    // ---------------- combine the warps' (m, l, M' - m, acc)
     __syncthreads();  // the slots of the part before are read
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -642,7 +647,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
       for (int j = 0; j < 2; ++j) {
         const int r = 8 * n + 2 * t + j;
         const float ls = col_sum(l[2 * n + j]);
-        if (g == 0) ml[warp * kRows + r] = make_float4(m[2 * n + j], ls, mv[2 * n + j], 0.f);
+        if (g == 0) ml[warp * kRows + r] = make_float4(m[2 * n + j], ls, dv[2 * n + j], 0.f);
         if (any) {
           float* dst = slots + ((size_t)warp * kRows + r) * kPad;
 #pragma unroll
@@ -664,28 +669,33 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
       const int i = query_of(r);
       __nv_bfloat16* dst = a.o + p.b * a.os + (long long)(p.h * a.G + r - i * a.G) * a.oh +
                            (long long)i * a.ot + 4 * lane;
-      const float f = st.y == 0.f ? 0.f : ex2_approx(st.z - st.x) / st.y;
+      const float f = st.y == 0.f ? 0.f : ex2_approx(st.z) / st.y;
       *reinterpret_cast<uint2*>(dst) =
           make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
     };
     // A part that saw nothing (a NaN sum is something) adds nothing.
     auto nothing = [](const float4& st) { return st.x == -INFINITY && st.y == 0.f; };
-    auto zero_if_inf = [](float x) { return x == -INFINITY ? 0.f : x; };
     for (int r = warp; r < rows; r += W + 1) {
       float4 st[W + 1], S = make_float4(-INFINITY, 0.f, -INFINITY, 0.f), o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w <= W; ++w) {
         st[w] = ml[w * kRows + r];
         S.x = fmaxf(S.x, st[w].x);
+      }
+      const float ref = or_zero(S.x);
+#pragma unroll
+      for (int w = 0; w <= W; ++w) {  // each from the common maximum
+        st[w].x -= ref;
+        st[w].z += st[w].x;
         S.z = fmaxf(S.z, st[w].z);
       }
-      const float ref = zero_if_inf(S.x), zref = zero_if_inf(S.z);
+      const float zref = or_zero(S.z);
 #pragma unroll
       for (int w = 0; w <= W; ++w) {
         if (nothing(st[w])) continue;
         const float f = ex2_approx(st[w].z - zref);
         const float4 v = *reinterpret_cast<const float4*>(slots + (w * kRows + r) * kPad + 4 * lane);
-        S.y += st[w].y * ex2_approx(st[w].x - ref);
+        S.y += st[w].y * ex2_approx(st[w].x);
         o.x += v.x * f;
         o.y += v.y * f;
         o.z += v.z * f;
@@ -729,22 +739,23 @@ __global__ void __launch_bounds__((W + 1) * 32, 1) quant_decode_kernel(QuantAttn
           for (int k = 0; k < kFirst; ++k)
             if (k < nc) u[k] = __ldcg(place(k) + 1 + lane);
           if (lane < nc) v = __ldcg(place(lane));
-          S.x = v.x;
-          S.z = v.z;
+          auto join = [&](float x, float z) {
+            const float xn = fmaxf(S.x, x), r = or_zero(xn);
+            S.z = fmaxf(S.x - r + S.z, x - r + z);
+            S.x = xn;
+          };
+          join(v.x, v.z);
           for (int k = lane + 32; k < nc; k += 32) {
             const float4 y = __ldcg(place(k));
-            S.x = fmaxf(S.x, y.x);
-            S.z = fmaxf(S.z, y.z);
+            join(y.x, y.z);
           }
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) {
-            S.x = fmaxf(S.x, __shfl_xor_sync(0xffffffffu, S.x, d));
-            S.z = fmaxf(S.z, __shfl_xor_sync(0xffffffffu, S.z, d));
-          }
-          const float ref = zero_if_inf(S.x), zref = zero_if_inf(S.z);
+          for (int d = 16; d > 0; d >>= 1)
+            join(__shfl_xor_sync(0xffffffffu, S.x, d), __shfl_xor_sync(0xffffffffu, S.z, d));
+          const float ref = or_zero(S.x), zref = or_zero(S.z);
           for (int k = lane; k < nc; k += 32) {
             if (k >= 32) v = __ldcg(place(k));
-            wt[k] = ex2_approx(v.z - zref);
+            wt[k] = ex2_approx(v.x - ref + v.z - zref);
             S.y += v.y * ex2_approx(v.x - ref);
           }
 #pragma unroll

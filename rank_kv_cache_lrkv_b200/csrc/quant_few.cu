@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
       const bool valid = r < R;
       const int pos = valid ? pos0 + r / a.G : 0x7fffffff;
       const int mine = (n - gr + 1) >> 1;  // steps of this group
-      float m = -INFINITY, l = 0.f, mv = -INFINITY, fcol = 0.f;
+      float m = -INFINITY, l = 0.f, dv = -INFINITY, fcol = 0.f;
       if (gr == 0) {
         // ---- q, as in quant_prefill.cu; a copy's rows are the unit's
         if (np > 0) quant_wait_warp(qempty, (np - 1) & 1, fail, lane);
@@ -328,17 +328,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
           }
           x0 = fmaxf(x0, x1);
         }
-        const float mn = x0 == -INFINITY ? x0 : x0 * fabsf(f);
-        const float vn = mn + ev;
+        const float mn = x0 == -INFINITY ? x0 : floorf(x0 * fabsf(f));
         if (mn > m + kLazy) {  // also from -inf
-          l *= ex2_approx(m - mn);
+          const float sh = m - mn;
+          l *= ex2_approx(sh);
+          dv += sh;
           m = mn;
         }
-        const bool grow = vn > mv + kLazy;
+        const float ref = or_zero(m), en = mn - ref + ev;
+        const bool grow = en > dv + kLazy;
         if (__any_sync(0xffffffffu, grow)) {
-          const float cr = grow ? ex2_approx(mv - vn) : 1.f;
-          if (grow) mv = vn;
-          if (__any_sync(0xffffffffu, fabsf(or_zero(mv)) > kWideRef)) fcol = -fabsf(fcol);
+          const float cr = grow ? ex2_approx(dv - en) : 1.f;
+          if (grow) dv = en;
+          if (__any_sync(0xffffffffu, fabsf(ref) > kWideRef)) fcol = -fabsf(fcol);
           if (k > 0 && quant_wait_warp(&odone[gr], (ns + k - 1) & 1, fail, lane)) {
             tc_fence_after();
 #pragma unroll 1
@@ -351,8 +353,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
             }
           }
         }
-        const float ref = or_zero(m), vref = or_zero(mv);
-        const float wm = fv * ex2_approx(ref - vref + ev + kBoostLog);
+        const float dref = or_zero(dv);
+        const float wm = fv * ex2_approx(ev - dref + kBoostLog);
         const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f), nref = make_float2(-ref, -ref);
         float2 sum = make_float2(0.f, 0.f);
         auto weigh = [&](auto edge_c) {
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
         };
         if (fcol < 0.f || sc.ok == kWideStep)
           sum.x = weigh_wide(tS, tP + copy * (CW / 2), CW, fabsf(f), !edge ? CW : sc.ok ? pos - base : -1, ref,
-                             ref - vref + ev + kBoostLog, fv);
+                             ev - dref + kBoostLog, fv);
         else if (edge)
           weigh(std::true_type());
         else
@@ -394,12 +396,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
         const int i = 2 * nfull + gr, at = (done + i) % kFewScales;
         tc_fence_after();
         if (gr == 1 && nfull == 0) fcol = fc[row];
-        const RowState st = open_step({m, l, mv}, tS, tP + copy * (CW / 2), tO, CW,
+        const RowState st = open_step({m, l, dv}, tS, tP + copy * (CW / 2), tO, CW,
                                       sm + pl.tok + at * kTokBytes + copy * CW * 2, fabsf(fcol),
                                       pos - (p.j0 + i) * kStepKeys - copy * CW,
                                       nfull > 0 ? &odone[gr] : nullptr, (ns + nfull - 1) & 1, fail);
         m = st.m;
-        mv = st.mv;
+        dv = st.dv;
         l = st.l;
         tmem_wait_st();
         tc_fence_before();
@@ -413,25 +415,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) quant_few_kernel(QuantAttnArgs
       done += n;
       ++np;
       // ---- the copies and groups of a row, 32 dims at a time
-      ml[tid] = make_float4(m, l, mv, 0.f);
+      ml[tid] = make_float4(m, l, dv, 0.f);
       named_bar(1, 256);
-      float Z = -INFINITY;
+      float M = -INFINITY, Z = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 2 * REP; ++i) Z = fmaxf(Z, ml[i * kCopy + r].z);
-      const float zref = Z == -INFINITY ? 0.f : Z;
-      const float mix = ex2_approx(mv - zref);
+      for (int i = 0; i < 2 * REP; ++i) M = fmaxf(M, ml[i * kCopy + r].x);
+      const float mref = or_zero(M);
+#pragma unroll
+      for (int i = 0; i < 2 * REP; ++i) Z = fmaxf(Z, ml[i * kCopy + r].x - mref + ml[i * kCopy + r].z);
+      const float mix = ex2_approx(m - mref + dv - or_zero(Z));
       const bool whole = p.j0 == 0 && p.j1 == p.steps;
       if (tid < kCopy) {
-        float M = -INFINITY, ls = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2 * REP; ++i) M = fmaxf(M, ml[i * kCopy + r].x);
-        const float mref = M == -INFINITY ? 0.f : M;
+        float ls = 0.f;
 #pragma unroll
         for (int i = 0; i < 2 * REP; ++i) {
           const float4 t = ml[i * kCopy + r];
           if (!(t.x == -INFINITY && t.y == 0.f)) ls += t.y * ex2_approx(t.x - mref);
         }
-        rowst[r] = make_float4(M, ls, Z, ls == 0.f ? 0.f : ex2_approx(Z - M - kBoostLog) / ls);
+        rowst[r] = make_float4(M, ls, Z, ls == 0.f ? 0.f : ex2_approx(Z - kBoostLog) / ls);
       }
       float4* rec = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.ws) + pre_records(gridDim.x)) +
                     ((size_t)2 * blockIdx.x + (p.j0 == 0 ? 1 : 0)) * kPreRecord;

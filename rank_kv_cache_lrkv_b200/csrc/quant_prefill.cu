@@ -40,7 +40,7 @@
 // against 1.23, 8K prompt 0.72 against 0.66.
 // A row keeps its references m (scores) and M' (scores + floor(log2 s_v)) as
 // long as they lag by at most 2^kLazy, so O is seldom rescaled; a weight is
-// then at most 2^(1 + kLazy + kBoostLog) = 2^15 and fp16's floor lies 2^-33
+// then under 2^(2 + kLazy + kBoostLog) = 2^15 and fp16's floor lies 2^-33
 // below the row's largest.
 //
 // The steps of all tiles are laid end to end and each CTA takes an equal
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       __syncwarp();
     }
     for (long long x = lo; x < hi;) {
-      float m = -INFINITY, l = 0.f, mv = -INFINITY, fcol = 0.f;
+      float m = -INFINITY, l = 0.f, dv = -INFINITY, fcol = 0.f;
       int pos;
       {
         const PrePart p = parts[warp];
@@ -443,17 +443,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
             }
             x0 = fmaxf(x0, x1);
           }
-          const float mn = x0 == -INFINITY ? x0 : x0 * fabsf(f);
-          const float vn = mn + ev;
+          const float mn = x0 == -INFINITY ? x0 : floorf(x0 * fabsf(f));
           if (mn > m + kLazy) {  // also from -inf
-            l *= ex2_approx(m - mn);
+            const float sh = m - mn;
+            l *= ex2_approx(sh);
+            dv += sh;
             m = mn;
           }
-          const bool grow = vn > mv + kLazy;
+          const float ref = or_zero(m), en = mn - ref + ev;
+          const bool grow = en > dv + kLazy;
           if (__any_sync(0xffffffffu, grow)) {
-            const float cr = grow ? ex2_approx(mv - vn) : 1.f;
-            if (grow) mv = vn;
-            if (__any_sync(0xffffffffu, fabsf(or_zero(mv)) > kWideRef)) fcol = -fabsf(fcol);
+            const float cr = grow ? ex2_approx(dv - en) : 1.f;
+            if (grow) dv = en;
+            if (__any_sync(0xffffffffu, fabsf(ref) > kWideRef)) fcol = -fabsf(fcol);
             // the step before has been added; this one waits for P
             if (i > 0 && quant_wait_warp(&odone[gr], (nd + i - 1) & 1, fail, lane)) {
               tc_fence_after();
@@ -467,9 +469,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
               }
             }
           }
-          const float ref = or_zero(m), vref = or_zero(mv);
+          const float dref = or_zero(dv);
           // 2^(m - M') s_v 2^kBoostLog
-          const float wm = fv * ex2_approx(ref - vref + ev + kBoostLog);
+          const float wm = fv * ex2_approx(ev - dref + kBoostLog);
           const float2 w2 = make_float2(wm, wm), f2 = make_float2(f, f), nref = make_float2(-ref, -ref);
           float2 sum = make_float2(0.f, 0.f);
           auto weigh = [&](auto edge_c) {
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
           };
           if (fcol < 0.f || sc.ok == kWideStep)
             sum.x = weigh_wide(tSb, tSb, kStepKeys, fabsf(f), !edge ? kStepKeys : sc.ok ? pos - base : -1, ref,
-                               ref - vref + ev + kBoostLog, fv);
+                               ev - dref + kBoostLog, fv);
           else if (edge)
             weigh(std::true_type());
           else
@@ -520,12 +522,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
         if (quant_wait_warp(&sfull[2 * gr + sb], (ns >> sb) & 1, fail, lane)) {
           ns ^= 1u << sb;
           tc_fence_after();
-          const RowState r = open_step({m, l, mv}, tSb, tSb, tO, kStepKeys, sm + pl.tok + at * kTokBytes,
+          const RowState r = open_step({m, l, dv}, tSb, tSb, tO, kStepKeys, sm + pl.tok + at * kTokBytes,
                                        fabsf(fcol), pos - (p.j0 + nopen) * kStepKeys,
                                        nopen > 0 ? &odone[gr] : nullptr, (nd + nopen - 1) & 1, fail);
           m = r.m;
           l = r.l;
-          mv = r.mv;
+          dv = r.dv;
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&pfull[2 * gr + sb]);
@@ -534,9 +536,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) quant_prefill_kernel(QuantAttn
       if (p.j1 > p.j0) {
       float4* records = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.ws) + pre_records(gridDim.x));
       const bool whole = p.j0 == 0 && p.j1 == p.steps;
-      const float4 st = make_float4(m, l, mv, 0.f);
+      const float4 st = make_float4(m, l, dv, 0.f);
       float4* rec = records + ((size_t)2 * blockIdx.x + (p.j0 == 0 ? 1 : 0)) * kPreRecord + gr * 128 + row;
-      const float fin = l == 0.f ? 0.f : ex2_approx(mv - m - kBoostLog) / l;
+      const float fin = l == 0.f ? 0.f : ex2_approx(dv - kBoostLog) / l;
       if (n > 0) {
         // (a barrier of its own: of odone's phases the last two may still be
         // open here, and a wait by parity tells only one from the one before)
@@ -851,10 +853,10 @@ __global__ void __launch_bounds__(256) quant_merge_kernel(QuantAttnArgs a, int C
   for (int cc = c0; cc <= cut.w; ++cc) {
     const float4 t = __ldcg(part(cc)), s = __ldcg(part(cc) + (size_t)(1 + lane) * kTileRows);
     if (t.x == -INFINITY && t.y == 0.f) continue;  // saw nothing (a NaN sum is something)
-    const float mn = fmaxf(M, t.x), mr = mn == -INFINITY ? 0.f : mn;
-    const float zn = fmaxf(Z, t.z), zr = zn == -INFINITY ? 0.f : zn;
-    l = l * ex2_approx(M - mr) + t.y * ex2_approx(t.x - mr);
-    const float f0 = ex2_approx(Z - zr), f1 = ex2_approx(t.z - zr);
+    const float mn = fmaxf(M, t.x), mr = or_zero(mn), a0 = M - mr, a1 = t.x - mr;
+    const float z0 = Z + a0, z1 = t.z + a1, zn = fmaxf(z0, z1), zr = or_zero(zn);  // M' from mn
+    l = l * ex2_approx(a0) + t.y * ex2_approx(a1);
+    const float f0 = ex2_approx(z0 - zr), f1 = ex2_approx(z1 - zr);
     M = mn;
     Z = zn;
     o.x = o.x * f0 + s.x * f1;
@@ -862,7 +864,7 @@ __global__ void __launch_bounds__(256) quant_merge_kernel(QuantAttnArgs a, int C
     o.z = o.z * f0 + s.z * f1;
     o.w = o.w * f0 + s.w * f1;
   }
-  const float f = l == 0.f ? 0.f : ex2_approx(Z - M - kBoostLog) / l;
+  const float f = l == 0.f ? 0.f : ex2_approx(Z - kBoostLog) / l;
   __nv_bfloat16* dst = a.o + b * a.os + (long long)(h * a.G + rr % a.G) * a.oh + (long long)(rr / a.G) * a.ot;
   *reinterpret_cast<uint2*>(dst + 4 * lane) =
       l == 0.f ? make_uint2(0, 0)

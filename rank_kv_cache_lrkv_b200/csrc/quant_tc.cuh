@@ -13,7 +13,7 @@ constexpr int kTileBytes = 2 * kKHalf;          // a step's keys, or its values 
 constexpr int kTileRows = 256;                  // rows of a record
 // References lag by at most 2^kLazy, weights carry 2^kBoostLog (see
 // quant_prefill.cu).
-constexpr float kLazy = 6.f;
+constexpr float kLazy = 5.f;
 constexpr float kBoostLog = 8.f;
 
 struct alignas(16) StepScales {
@@ -29,7 +29,7 @@ constexpr int kTokValues = 2 * kStepKeys, kTokBytes = 2 * kTokValues;
 // Workspace: the counters of the few-row kernel (not used here, and left
 // alone), a cut per CTA (sequence, head, row and last CTA of the tile that
 // begins in it and goes on elsewhere; last CTA -1: none), two records per CTA
-// as in quant_decode.cu, of [33][256] float4: (m, l, M', -) of a row, then its
+// as in quant_decode.cu, of [33][256] float4: (m, l, M' - m, -) of a row, then its
 // 128 sums four at a time, rows side by side.
 constexpr size_t kPreRecord = (size_t)33 * kTileRows;
 __host__ __device__ inline size_t pre_cuts(int C) { return ((size_t)C * 4 + 255) / 256 * 256; }
@@ -242,20 +242,22 @@ static __device__ __noinline__ void open_values(const __nv_bfloat16* rows, int n
 
 // ---- the softmax of the open block, and of a step whose exponents are far apart
 //
-// The usual step weighs with v = 2^(s f - m) and v (2^(m - M') s_v 2^kBoostLog).
-// That takes two things, and a step that lacks either is weighed by weigh_wide
-// (a real function over S in TMEM: it is seldom called):
+// A row holds m, the largest score rounded down, and M' - m (M' as in
+// quant_decode.cu): whole numbers, exact however large the scores are.  The usual
+// step weighs with v = 2^(s f - m) and v (2^(m - M') s_v 2^kBoostLog).  That takes two
+// things, and a step that lacks either is weighed by weigh_wide (a real function
+// over S in TMEM: it is seldom called):
 //  * 2^(m - M') s_v small, as v is flushed under 2^-126.  M' is at most kLazy under m +
 //    log2 of the value scale where m was found, so with all scales of a part in
 //    [2^-35, 2^35] the factor is at most 2^(70 + kLazy + 1 + kBoostLog), and weights
-//    under 2^-41 are flushed (half of fp16's smallest step is 2^-25).  The
+//    under 2^-42 are flushed (half of fp16's smallest step is 2^-25).  The
 //    converters mark a step whose scale is above that range, or whose part had one
 //    below it (wide_step).
-//  * |m| small: m is s f rounded and s f in the fma is not, so v is off by 2 to half
-//    an ulp of m, alike for all tokens of a row; from 2^24 on a weight could
-//    overflow.  |M'| tells (it moves with m) and is looked at where it moves; a warp
-//    with such a row has its factors fcol negated for the rest of the part.  (What multiplies v takes m - M' first:
-//    that is exact.)
+//  * |m| small: s f is not rounded in the fma, but m comes from it rounded, so v is
+//    off by 2 to half an ulp of the score, alike for all tokens of a row; from 2^24
+//    on a weight could overflow.  m is looked at where M' moves (it cannot move far
+//    alone); a warp with such a row has its factors fcol negated for the rest of the
+//    part.
 constexpr int kWideStep = 2;
 constexpr float kWideRef = 1048576.f;
 // StepScales::ok of a full block; low: it, or a block of its part before it, was under the range.
@@ -263,7 +265,6 @@ __device__ __forceinline__ int wide_step(float sv, bool& low) {
   low |= sv < 2.9103830456733704e-11f;               // 2^-35
   return low || sv > 34359738368.f ? kWideStep : 1;  // 2^35
 }
-__device__ __forceinline__ float or_zero(float x) { return x == -INFINITY ? 0.f : x; }
 // Weights of the columns of S up to `last` (0 behind it) to TMEM at tP, which may be
 // where S is; returns their sum.  c: log2 of what p is multiplied by, beside fv.
 static __device__ __noinline__ float weigh_wide(uint32_t tS, uint32_t tP, int columns, float f, int last,
@@ -293,36 +294,48 @@ static __device__ __noinline__ float weigh_wide(uint32_t tS, uint32_t tP, int co
 // (whose last sums `odone` tells of; nullptr: there are none yet).  tok: the
 // columns' tokens, fcol: the row's factor.
 struct RowState {
-  float m, l, mv;
+  float m, l, dv;
 };
 static __device__ __noinline__ RowState open_step(RowState r, uint32_t tS, uint32_t tP, uint32_t tO,
                                                   int columns, const uint8_t* tok, float fcol, int last,
                                                   uint64_t* odone, uint32_t parity, volatile int* fail) {
   // scores, back to where S was (masked: -inf); the largest, and the largest score +
-  // exponent of the value
-  float mn = -INFINITY, vn = -INFINITY;
+  // exponent of the value, from a whole number `at` that follows the scores
+  float mn = -INFINITY, vn = -INFINITY, at = or_zero(r.m);
 #pragma unroll 1
   for (int k0 = 0; k0 < columns; k0 += 8) {
     uint32_t s[8];
     tmem_ld8(tS + k0, s);
     const Tok8 ev(tok + 2 * k0), kf(tok + kTokValues + 2 * k0);
+    float x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      float x = __fmul_rn(__uint_as_float(s[k]), fcol * kf[k]);
-      if (k0 + k > last) x = -INFINITY;
-      mn = fmaxf(mn, x);
-      vn = fmaxf(vn, x + ev[k]);
-      s[k] = __float_as_uint(x);
+      x[k] = k0 + k > last ? -INFINITY : __fmul_rn(__uint_as_float(s[k]), fcol * kf[k]);
+      mn = fmaxf(mn, x[k]);
+      s[k] = __float_as_uint(x[k]);
     }
     tmem_st8(tS + k0, s);
+    const float to = floorf(mn);
+    if (to > -INFINITY) {
+      vn += at - to;
+      at = to;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) vn = fmaxf(vn, x[k] - at + ev[k]);
   }
+  mn = floorf(mn);
   if (mn > r.m + kLazy) {
-    r.l *= ex2_approx(r.m - mn);
+    const float sh = r.m - mn;
+    r.l *= ex2_approx(sh);
+    r.dv += sh;
     r.m = mn;
   }
-  const bool grow = vn > r.mv + kLazy;
-  const float cr = grow ? ex2_approx(r.mv - vn) : 1.f;
-  if (grow) r.mv = vn;
+  const float ref = or_zero(r.m);
+  vn += at - ref;
+  vn = floorf(vn);
+  const bool grow = vn > r.dv + kLazy;
+  const float cr = grow ? ex2_approx(r.dv - vn) : 1.f;
+  if (grow) r.dv = vn;
   if (__any_sync(0xffffffffu, grow) && odone && quant_wait_warp(odone, parity, fail, threadIdx.x & 31)) {
     tc_fence_after();
 #pragma unroll 1
@@ -335,7 +348,7 @@ static __device__ __noinline__ RowState open_step(RowState r, uint32_t tS, uint3
     }
   }
   tmem_wait_st();
-  const float ref = or_zero(r.m), c = ref - or_zero(r.mv) + kBoostLog;
+  const float c = kBoostLog - or_zero(r.dv);
   float sum = 0.f;
 #pragma unroll 1
   for (int k0 = 0; k0 < columns; k0 += 8) {

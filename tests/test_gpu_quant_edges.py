@@ -292,3 +292,27 @@ def test_scores_of_minus_infinity_alone(lrkv, G, n):
     q[..., 7] = 2
     assert not _attend(lrkv, cache, q).any()
     assert cache.error() == 0
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,n", CALLS)
+def test_scores_of_millions_with_values_of_any_size(lrkv, code, G, n):
+    """The exponent of the values does not get lost next to a large score."""
+    L = 150
+    c = np.full(L, 0.5)
+    c[[0, 100, 140]] = [1, 2, 4]
+    for gain in (2.0 ** 20, 2.0 ** 21, 2.0 ** 22, 2.0 ** 23, 2.0 ** 24, 2.0 ** 60):
+        for size in (-60, -30, -9, -5, -3, -1, 3, 7, 40, 90):
+            v = _rows(2, 1, 1, L, 0.0) * 2.0 ** size
+            k, q = _along(c, n, gain)
+            cache = lrkv.QuantCache(1, 1, L, code=code)
+            oc = qo.QuantCacheOracle(1, 1, code)
+            _write(cache, oc, lrkv, k[None, None], v)
+            got = _attend(lrkv, cache, q[None, None].expand(1, G, n, 128).contiguous())[0]
+            V = oc.values(0, 0, 1)
+            for i in range(n):
+                pos = L - n + i
+                want = V[140 if pos >= 140 else 100 if pos >= 100 else 0]
+                # as in test_scores_of_millions
+                tol = np.abs(want) * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20)
+                assert (np.abs(got[:, i] - want) <= tol).all(), (gain, size, i)
