@@ -316,3 +316,42 @@ def test_scores_of_millions_with_values_of_any_size(lrkv, code, G, n):
                 # as in test_scores_of_millions
                 tol = np.abs(want) * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20)
                 assert (np.abs(got[:, i] - want) <= tol).all(), (gain, size, i)
+
+
+@pytest.mark.parametrize("G,n", CALLS)
+@pytest.mark.parametrize("scale", [0.0, -SCALE])
+def test_scales_that_are_not_positive(lrkv, G, n, scale):
+    L = 64 * 3 + 45
+    cache = lrkv.QuantCache(1, 2, L)
+    oc = qo.QuantCacheOracle(1, 2, "int8")
+    _write(cache, oc, lrkv, _rows(1, 1, 2, L), _rows(2, 1, 2, L))
+    q = _rows(3, 1, 2 * G, n, 0.0)
+    o = torch.zeros_like(q, device="cuda")
+    lrkv.quant_attn(cache, q.cuda(), scale, o, lrkv.quant_attn_workspace(cache, 2 * G, n))
+    ref, tol = _bound(oc, q[0].double().numpy() * (scale / SCALE), n, G)
+    assert (np.abs(o[0].double().cpu().numpy() - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("G,n", CALLS)
+def test_shared_queries_and_rows_of_a_wider_buffer(lrkv, G, n):
+    """q with strides of 0 (one row for all heads and sequences); o's rows apart,
+    what lies between them untouched."""
+    B, H, L = 3, 2, 150
+    cache = lrkv.QuantCache(B, H, L, code="e4m3")
+    k, v = _rows(1, B, H, L), _rows(2, B, H, L)
+    lrkv.quant_append(cache, k.cuda(), v.cuda())
+    one = _rows(3, 1, 1, n, 0.0).cuda()
+    q = one.expand(B, H * G, n, 128)
+    wide = torch.full((B, n, H * G, 136), 3.0, dtype=torch.bfloat16, device="cuda")
+    o = wide[..., :128].transpose(1, 2)
+    ws = lrkv.quant_attn_workspace(cache, H * G, n)
+    lrkv.quant_attn(cache, q, SCALE, o, ws)
+    assert bool((wide[..., 128:] == 3.0).all())
+    want = torch.zeros(B, H * G, n, 128, dtype=torch.bfloat16, device="cuda")
+    lrkv.quant_attn(cache, q.contiguous(), SCALE, want, ws)
+    assert torch.equal(o, want)
+    for b in range(B):
+        oc = qo.QuantCacheOracle(1, H, "e4m3")
+        oc.append(k[b:b + 1].double().numpy(), v[b:b + 1].double().numpy())
+        ref, tol = _bound(oc, q[b].double().cpu().numpy(), n, G)
+        assert (np.abs(o[b].double().cpu().numpy() - ref) <= tol).all()
