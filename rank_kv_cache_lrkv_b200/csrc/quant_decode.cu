@@ -15,13 +15,13 @@
 //
 // What bounds it (calls over several caches in turn, more than L2 holds, at the
 // clock named): HBM for long caches (64 sequences of 12,288 tokens x 8 heads: 1.6 GB
-// in 246 us at 1,965 MHz, 286 in a long run at 1,700; 4 of 32,769: 50 us, 5,390 GB/s
-// at 1,940), latency for short ones: 8 to 9 us between the launch and the last part
-// folded (512 tokens 8.5 us, 4 x 8192 19.8 us, both at 1,965 MHz).  With 9 to 16 rows
-// no pipe is full (issue slots 34 %, warp MMAs 18 %, DRAM 39 %): a warp's only slab is
+// in 244 us at 1,965 MHz, 280 in a long run at 1,670; 4 of 32,769: 50 us, 5,350 GB/s
+// at 1,930), latency for short ones: 8 to 9 us between the launch and the last part
+// folded (512 tokens 8.4 us, 4 x 8192 19.8 us, both at 1,965 MHz).  With 9 to 16 rows
+// no pipe is full (issue slots 34 %, warp MMAs 18 %, DRAM 40 %): a warp's only slab is
 // empty while its next page comes, and its page takes it a chain of products,
-// exponentials and products.  8 sequences of 12,288, 16 rows: 56 us int8, 52 e4m3
-// (3,580 and 3,860 GB/s, 1,965 MHz).
+// exponentials and products.  8 sequences of 12,288, 16 rows: 57 us int8, 53 e4m3
+// (3,530 and 3,810 GB/s, 1,965 MHz).
 // Figures of one choice against another, below, are of calls back to back on one
 // cache, of which L2 keeps a part.
 //

@@ -14,8 +14,8 @@
 // What bounds it: the latency of a page's way through the roles (codes, tile,
 // S, P, O).  Two pages are under way at a time and one leaves every 0.85 us,
 // 1.25 with 128 rows; its bytes would take 0.37.  4 x 8 heads x 16,384 tokens
-// (134 MB, caches in turn, 1,965 MHz) with 20 rows 53 us, 32 rows 55, 64 rows 58,
-// 128 rows 78.
+// (134 MB, caches in turn, 1,930 to 1,965 MHz) with 20 rows 54 us, 32 rows 56,
+// 64 rows 59, 128 rows 78.
 //
 // Persistent, one CTA per SM, 18 warps, the pages of all units dealt evenly:
 //  * warp 17: one bulk copy per page slab into a ring of NR (44 bytes a

@@ -25,10 +25,10 @@
 // is the chain of a step through softmax (2000: TMEM's latency, the row
 // maximum, the exponentials, the hand-over) and back through the products.  And
 // the card: in a long run it draws 990 W, its limit, at 1.78 GHz of 1.965.
-// 2048 queries of 32 heads over 2 x 16,384 tokens: 1.05 ms (990 TFLOP/s) on a
+// 2048 queries of 32 heads over 2 x 16,384 tokens: 1.06 ms (970 TFLOP/s) on a
 // cool card at 1,965 MHz, 1.16 ms (885) in a long run at 1,800; 8192 over themselves
-// 0.61 to 0.65 ms (905 to 850).  A tile's start and end take 12 to 16 thousand
-// clocks: 32 prompts of 512 tokens 198 us (347 TFLOP/s, 1,965 MHz).
+// 0.61 to 0.65 ms (900 to 845).  A tile's start and end take 12 to 16 thousand
+// clocks: 32 prompts of 512 tokens 199 us (346 TFLOP/s, 1,965 MHz).
 // Measured against it, the 2048 queries: two threads a row on sixteen softmax
 // warps 1.38 ms against 1.09 (what a row costs once is paid twice); sixteen
 // warps that take a row's steps in turns 1.17 against 1.12; one S that is given

@@ -149,7 +149,7 @@ __device__ __forceinline__ void put_codes(uint8_t* rowp, int row, int cc, const 
 // the 128 threads ct of the converters.  Real functions: once a sequence at most,
 // and in line their registers and instructions cost every page (long calls 2 to 8 %).
 // Short ones: code that is run through a single time is waited for, 16 bytes an
-// instruction (64 rows of values unrolled, 168 prompts of 189 tokens 150 us, so 91).
+// instruction (64 rows of values unrolled, 168 prompts of 189 tokens 150 us, so 92).
 __device__ __forceinline__ uint32_t abs_max8(const uint4& w) {  // bf16 bits
   const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
                               __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
